@@ -15,6 +15,12 @@ Calls (same names as the C ABI, without the ``hysparse_`` prefix):
 * ``sparse_attn`` -- one sparse layer: global branch over the top-k keys,
   causal 128-token window branch, sigmoid gate; reuses the full layer's K/V.
 * ``block`` -- one full layer + top-k + N sparse layers.
+
+Around the paged caches that ``block_paged`` decodes over (module ``ragged``):
+
+* ``rope`` (and ``rope_frequencies``) -- rotary positions of q and k.
+* ``cache_write`` / ``cache_read`` -- new rows into the pages, plain or as 8-bit
+  floats, and rows back out of them.
 """
 from __future__ import annotations
 
@@ -26,10 +32,11 @@ import torch
 
 from . import _lib
 from ._lib import HysparseError, HsShape
+from .ragged import cache_read, cache_write, rope, rope_frequencies
 
 __all__ = ["shape_of", "workspace_size", "alloc_workspace", "full_attn_scores", "topk",
            "sparse_attn", "block", "block_paged", "workspace_status", "version", "launch_count",
-           "kv_cache_bytes", "HysparseError", "HsShape"]
+           "kv_cache_bytes", "rope", "rope_frequencies", "cache_write", "cache_read", "HysparseError", "HsShape"]
 
 
 def _dtype_code(t: torch.dtype) -> int:

@@ -22,6 +22,11 @@ HS_ERR_TIMEOUT = 6
 # hs_dtype
 HS_F32 = 0
 HS_BF16 = 1
+HS_E4M3 = 2
+
+# flags of the rotary calls
+HS_ROPE_INTERLEAVED = 1
+HS_ROPE_INVERSE = 2
 
 EXPORTS = (
     "hysparse_workspace_size",
@@ -34,6 +39,9 @@ EXPORTS = (
     "hysparse_block_varlen",
     "hysparse_block_paged",
     "hysparse_full_attn_scores_noalloc",
+    "hysparse_rope",
+    "hysparse_cache_write",
+    "hysparse_cache_read",
     "hysparse_workspace_status",
     "hysparse_probe_l2_read",
     "hysparse_launch_count",
@@ -46,6 +54,13 @@ class HsShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Lq", ctypes.c_int), ("Lkv", ctypes.c_int),
                 ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class HsPagedCache(ctypes.Structure):
+    _fields_ = [("cu_rows", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("cache_dtype", ctypes.c_int), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class HysparseError(RuntimeError):
@@ -89,6 +104,13 @@ def lib():
     L.hysparse_block_paged.restype = I
     L.hysparse_full_attn_scores_noalloc.argtypes = [SP, P, P, P, P, P, P, LL, I, I, P]
     L.hysparse_full_attn_scores_noalloc.restype = I
+    F, CP = ctypes.c_float, ctypes.POINTER(HsPagedCache)
+    L.hysparse_rope.argtypes = [I, I, I, I, I, P, LL, P, LL, P, P, I, I, F, P, LL, P, LL, P]
+    L.hysparse_rope.restype = I
+    L.hysparse_cache_write.argtypes = [CP, I, I, I, I, P, LL, P, LL, P, I, I, F, P, P]
+    L.hysparse_cache_write.restype = I
+    L.hysparse_cache_read.argtypes = [CP, P, I, I, I, I, P, P, P, P]
+    L.hysparse_cache_read.restype = I
     L.hysparse_probe_l2_read.argtypes = [P, SZ, I, I, I, P, P]
     L.hysparse_probe_l2_read.restype = I
     L.hysparse_launch_count.argtypes = []

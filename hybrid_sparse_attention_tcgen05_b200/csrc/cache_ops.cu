@@ -1,0 +1,459 @@
+// The memory-bound operators around the attention calls: rotary positions,
+// the write of new keys and values into paged caches (copied, or as 8-bit
+// floats under a power-of-two scale per row and head) and its counterpart
+// that reads rows back.  All three are bound by HBM: each input byte is read
+// once and each output byte written once, in 16-byte accesses.
+#include <atomic>
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ragged.cuh"
+
+namespace hs {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ rope
+
+struct RopeParams {
+    int T, Hq, Hkv, d, half;
+    long long ld_q, ld_k, ld_oq, ld_ok;
+    const void *q, *k;
+    void *oq, *ok;
+    const int32_t *positions;
+    const double *inv_freq;
+    float amp;
+    int inverse;
+    int units;      // units of one row that need work (pairs, and the part left as it is when it has to be copied)
+    int tokens;     // tokens a block takes
+};
+
+// One unit of a row: V pairs (first and second halves: 2 V elements) or V
+// neighbouring elements (V / 2 pairs), or V elements that are only copied.
+template <typename T, int V, bool INTER>
+struct RopeUnit {
+    float a[V], b[V];
+    const T *src;
+    T *dst;
+    int pair;       // first pair of the unit, < 0: copy
+    __device__ void load(const RopeParams &p, int t, int head, int u) {
+        if (head < p.Hq) {
+            src = (const T *)p.q + t * p.ld_q + (long long)head * p.d;
+            dst = (T *)p.oq + t * p.ld_oq + (long long)head * p.d;
+        } else {
+            src = (const T *)p.k + t * p.ld_k + (long long)(head - p.Hq) * p.d;
+            dst = (T *)p.ok + t * p.ld_ok + (long long)(head - p.Hq) * p.d;
+        }
+        const int at = u * V;
+        if (INTER) {
+            pair = at < 2 * p.half ? at / 2 : -1;
+            src += at;
+            dst += at;
+            load_n<V>(src, a);
+        } else if (at < p.half) {
+            pair = at;
+            src += at;
+            dst += at;
+            load_n<V>(src, a);
+            load_n<V>(src + p.half, b);
+        } else {
+            pair = -1;
+            src += at + p.half;   // units from half / V on are the rest, elements 2 * half ..
+            dst += at + p.half;
+            load_n<V>(src, a);
+        }
+    }
+    __device__ void store(const RopeParams &p, const float2 *cs) {
+        if (pair >= 0) {
+            if (INTER) {
+#pragma unroll
+                for (int e = 0; e + 1 < V; e += 2) {
+                    const float2 w = cs[pair + e / 2];
+                    const float x = a[e], y = a[e + 1];
+                    a[e] = rope_first(x, y, w);
+                    a[e + 1] = rope_second(x, y, w);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float2 w = cs[pair + e];
+                    const float x = a[e], y = b[e];
+                    a[e] = rope_first(x, y, w);
+                    b[e] = rope_second(x, y, w);
+                }
+                store_n<V>(dst + p.half, b);
+            }
+        }
+        store_n<V>(dst, a);
+    }
+};
+
+// The angles depend on the token and the pair only, so a block computes them
+// once for its tokens (in 64 bits, into shared memory) and turns all the
+// heads of q and k with them.  A unit is read whole before any of it is
+// written, so out may be the input itself.
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+    extern __shared__ float2 cs[];
+    const int t0 = blockIdx.x * p.tokens;
+    const int nt = min(p.tokens, p.T - t0);
+    for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
+        float2 w = rope_cs(__ldg(p.positions + t0 + i / p.half), p.inv_freq[i % p.half], p.amp);
+        if (p.inverse) w.y = -w.y;
+        cs[i] = w;
+    }
+    __syncthreads();
+    const int per_token = (p.Hq + p.Hkv) * p.units;
+    const int n = nt * per_token;
+    constexpr int BATCH = 2;
+    for (int i0 = (blockIdx.y * BATCH) * kThreads + threadIdx.x; i0 < n; i0 += BATCH * kThreads * gridDim.y) {
+        RopeUnit<T, V, INTER> w[BATCH];
+        int tok[BATCH];
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+            const int i = i0 + e * kThreads;
+            tok[e] = -1;
+            if (i < n) {
+                tok[e] = i / per_token;
+                const int r = i - tok[e] * per_token;
+                w[e].load(p, t0 + tok[e], r / p.units, r % p.units);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e)
+            if (tok[e] >= 0) w[e].store(p, cs + tok[e] * p.half);
+    }
+}
+
+template <typename T, int V, bool INTER>
+cudaError_t rope_go(RopeParams p, bool copy_rest, cudaStream_t st) {
+    p.units = INTER ? (copy_rest ? p.d : 2 * p.half) / V : (copy_rest ? p.d - p.half : p.half) / V;
+    const long long per_token = (long long)(p.Hq + p.Hkv) * p.units;
+    // one token a block while that leaves SMs idle, then four: fewer blocks,
+    // and the angles of four tokens fill the block's threads
+    p.tokens = p.T >= 4096 ? 4 : 1;
+    const int blocks = (p.T + p.tokens - 1) / p.tokens;
+    const long long n = per_token * p.tokens;
+    int y = (int)((n + 2 * kThreads - 1) / (2 * kThreads));
+    if (blocks >= 592) y = 1;          // four blocks an SM: the heads need no further split
+    y = y < 1 ? 1 : (y > 8 ? 8 : y);
+    rope_kernel<T, V, INTER><<<dim3(blocks, y), kThreads, p.tokens * p.half * sizeof(float2), st>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t rope_typed(const RopeParams &p, bool interleaved, bool copy_rest, cudaStream_t st) {
+    constexpr int W = 16 / (int)sizeof(T);
+    // the widest access that the pairs' layout allows: 16 bytes where the
+    // rotated part (or each half of it) is a multiple of that
+    const int unit = interleaved ? 2 * p.half : p.half;
+    if (interleaved) {
+        if (unit % W == 0) return rope_go<T, W, true>(p, copy_rest, st);
+        return rope_go<T, 2, true>(p, copy_rest, st);
+    }
+    if (unit % W == 0) return rope_go<T, W, false>(p, copy_rest, st);
+    if (unit % 4 == 0) return rope_go<T, 4, false>(p, copy_rest, st);
+    return rope_go<T, 1, false>(p, copy_rest, st);
+}
+
+// ------------------------------------------------------------------ cache write
+
+struct WriteParams {
+    PagedCache c;
+    int T, Hkv, d, half;          // half: rotated pairs of a key (0: none)
+    long long ld_k, ld_v;
+    const void *k, *v;
+    const double *inv_freq;
+    float amp;
+    int interleaved;
+    unsigned int *status;
+    int tokens;                    // tokens a block takes
+};
+
+// Eight elements of a row from element e0 on, rotated when they lie in the
+// rotated part (d and e0 are multiples of 8).  The partners of the first half
+// lie `half` further, those of the second half `half` back; they come from
+// the row just read (L1).
+template <typename T>
+__device__ __forceinline__ void load_row8(const T *row, int e0, int half, bool inter, const float2 *cs, float (&x)[8]) {
+    load_n<8>(row + e0, x);
+    if (e0 >= 2 * half) return;
+    if (inter) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            if (e0 + i < 2 * half) {
+                const float2 w = cs[(e0 + i) / 2];
+                const float a = x[i], b = x[i + 1];
+                x[i] = rope_first(a, b, w);
+                x[i + 1] = rope_second(a, b, w);
+            }
+        }
+        return;
+    }
+    if ((half & 7) == 0) {
+        const bool first = e0 < half;
+        float y[8];
+        load_n<8>(row + (first ? e0 + half : e0 - half), y);
+        const float2 *w = cs + (first ? e0 : e0 - half);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = first ? rope_first(x[i], y[i], w[i]) : rope_second(y[i], x[i], w[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = e0 + i;
+        if (e < half) x[i] = rope_first(x[i], Elem<T>::to_f(row[e + half]), cs[e]);
+        else if (e < 2 * half) x[i] = rope_second(Elem<T>::to_f(row[e - half]), x[i], cs[e - half]);
+    }
+}
+
+// The exponent byte (e + 127) of the smallest power of two 2^e with
+// amax <= 448 * 2^e, 448 being the largest 8-bit float; 2^0 for a row of
+// zeros.  448 = 1.75 * 2^8, so e follows from amax's own exponent and from
+// whether its mantissa is above 1.75.
+__device__ __forceinline__ int scale_byte(float amax) {
+    if (!(amax > 0.f)) return 127;
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < 1 ? 1 : e;
+}
+
+// One group of lanes per (token, K or V, head) row, eight elements a lane.
+// 8-bit rows: the group's largest magnitude gives the scale, a power of two,
+// so that dividing by it is exact and the 8-bit float is the only rounding
+// (by at most 2^-4 of the value); every reader can widen such a value to bf16
+// exactly.
+template <typename TI, typename TO, bool Q8>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams p) {
+    extern __shared__ float2 cs[];
+    __shared__ long long slot[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * p.tokens;
+    const int nt = min(p.tokens, p.T - t0);        // tokens <= 8: one warp finds each token's place
+    __shared__ int at[8];
+    if (warp < nt) {
+        int b = 0;
+        const long long pos = cache_position(p.c, p.T, t0 + warp, p.status, &b);
+        const long long r = pos < 0 ? -1 : pool_row(p.c, b, pos, p.status);
+        if (lane == 0) {
+            slot[warp] = r;
+            at[warp] = (int)pos;
+        }
+    }
+    __syncthreads();
+    if (p.half > 0) {
+        for (int i = threadIdx.x; i < nt * p.half; i += kThreads)
+            if (slot[i / p.half] >= 0) cs[i] = rope_cs(at[i / p.half], p.inv_freq[i % p.half], p.amp);
+        __syncthreads();
+    }
+    const int lanes = p.d / 8;                                    // lanes that hold the row
+    const int group = lanes <= 1 ? 1 : 1 << (32 - __clz(lanes - 1));   // rounded up to a power of two (<= 32)
+    const int sub = threadIdx.x & (group - 1);
+    const int per = kThreads / group;                             // rows a block handles at a time
+    const int rows = nt * 2 * p.Hkv;
+    for (int r0 = 0; r0 < rows; r0 += per) {
+        const int r = r0 + threadIdx.x / group;
+        const int tok = r / (2 * p.Hkv);
+        const int kh = r - tok * 2 * p.Hkv;
+        const bool is_v = kh >= p.Hkv;
+        const int h = is_v ? kh - p.Hkv : kh;
+        const bool live = r < rows && sub < lanes && slot[min(tok, nt - 1)] >= 0;
+        float x[8];
+        if (live) {
+            const TI *row = is_v ? (const TI *)p.v + (long long)(t0 + tok) * p.ld_v + h * p.d
+                                 : (const TI *)p.k + (long long)(t0 + tok) * p.ld_k + h * p.d;
+            load_row8(row, sub * 8, is_v ? 0 : p.half, p.interleaved != 0, cs + tok * p.half, x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.f;
+        }
+        [[maybe_unused]] int byte = 127;
+        if constexpr (Q8) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+            for (int o = group >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            byte = scale_byte(m);
+        }
+        if (!live) continue;
+        const long long dst_row = slot[tok];
+        const size_t o = ((size_t)dst_row * p.Hkv + h) * p.d + sub * 8;
+        if constexpr (Q8) {
+            const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);    // 2^-e, e <= 120
+            uint2 w;
+            __nv_fp8x2_storage_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE,
+                                                __NV_E4M3);
+            w.x = (uint32_t)c[0] | ((uint32_t)c[1] << 16);
+            w.y = (uint32_t)c[2] | ((uint32_t)c[3] << 16);
+            *reinterpret_cast<uint2 *>((uint8_t *)(is_v ? p.c.v_pages : p.c.k_pages) + o) = w;
+            if (sub == 0) (is_v ? p.c.v_scale : p.c.k_scale)[scale_index(p.c, dst_row, p.Hkv, h)] = (uint8_t)byte;
+        } else {
+            store_n<8>((TO *)(is_v ? p.c.v_pages : p.c.k_pages) + o, x);
+        }
+    }
+}
+
+template <typename TI, typename TO, bool Q8>
+cudaError_t write_go(WriteParams p, cudaStream_t st) {
+    // two tokens a block once that still gives every SM its blocks
+    p.tokens = p.T >= 4096 ? 8 : (p.T >= 1024 ? 2 : 1);
+    cache_write_kernel<TI, TO, Q8><<<(p.T + p.tokens - 1) / p.tokens, kThreads,
+                                     (size_t)p.tokens * p.half * sizeof(float2), st>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ cache read
+
+struct ReadParams {
+    PagedCache c;
+    const int32_t *start;
+    int total, Hkv, d;
+    void *k, *v;
+    unsigned int *status;
+    int tokens;
+};
+
+constexpr int kReadTokens = 16;   // most packed rows a block takes
+
+// Sixteen elements of a cache row as floats (the row's power of two applied).
+template <typename TC>
+__device__ __forceinline__ void widen16(const TC *p, float, float (&x)[16]) {
+    float a[8], b[8];
+    load_n<8>(p, a);
+    load_n<8>(p + 8, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = a[i];
+        x[8 + i] = b[i];
+    }
+}
+__device__ __forceinline__ void widen16(const __nv_fp8_e4m3 *p, float scale, float (&x)[16]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        x[2 * i] = f.x * scale;
+        x[2 * i + 1] = f.y * scale;
+    }
+}
+
+// A scale byte's power of two.  Byte 0 would be 2^-127 (not a normal float)
+// and is never written here; it reads as that all the same.
+__device__ __forceinline__ float scale_of_byte(int byte) {
+    return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)byte << 23);
+}
+
+template <typename TC, typename TO, bool Q8>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p) {
+    __shared__ long long slot[kReadTokens];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * p.tokens;
+    const int nt = min(p.tokens, p.total - t0);
+    for (int i = warp; i < nt; i += kThreads / 32) {
+        const int row = t0 + i;
+        const int b = seq_of_row(p.c.cu_rows, p.c.B, row);
+        long long r = -1;
+        if (b >= 0 && row < __ldg(p.c.cu_rows + b + 1)) {
+            const long long pos = (long long)row - __ldg(p.c.cu_rows + b) + (p.start ? __ldg(p.start + b) : 0);
+            if (pos < 0 || pos >= ((long long)p.c.max_pages << p.c.page_shift)) report(p.status, HS_ERR_INVALID_ARG);
+            else r = pool_row(p.c, b, pos, p.status);
+        }
+        if (lane == 0) slot[i] = r;
+    }
+    __syncthreads();
+    const int units = p.d / 16;
+    const int n = nt * p.Hkv * units;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int tok = i / (p.Hkv * units);
+        const int rest = i - tok * p.Hkv * units;
+        const int h = rest / units, e0 = (rest - h * units) * 16;
+        const long long r = slot[tok];
+        if (r < 0) continue;
+        const size_t src = ((size_t)r * p.Hkv + h) * p.d + e0;
+        const size_t dst = ((size_t)(t0 + tok) * p.Hkv + h) * p.d + e0;
+        float ks = 1.f, vs = 1.f;
+        if (Q8) {
+            const size_t si = scale_index(p.c, r, p.Hkv, h);
+            ks = scale_of_byte(p.c.k_scale[si]);
+            vs = scale_of_byte(p.c.v_scale[si]);
+        }
+        float x[16], y[16];
+        widen16((const TC *)p.c.k_pages + src, ks, x);
+        widen16((const TC *)p.c.v_pages + src, vs, y);
+        float a[8], b[8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                a[e] = x[8 * half + e];
+                b[e] = y[8 * half + e];
+            }
+            store_n<8>((TO *)p.k + dst + 8 * half, a);
+            store_n<8>((TO *)p.v + dst + 8 * half, b);
+        }
+    }
+}
+
+template <typename TC, typename TO, bool Q8>
+cudaError_t read_go(ReadParams p, cudaStream_t st) {
+    p.tokens = p.total >= 8192 ? kReadTokens : (p.total >= 1024 ? 4 : 1);
+    cache_read_kernel<TC, TO, Q8><<<(p.total + p.tokens - 1) / p.tokens, kThreads, 0, st>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t rope_launch(const RopeCall &a, cudaStream_t st) {
+    RopeParams p{};
+    p.T = a.T; p.Hq = a.Hq; p.Hkv = a.Hkv; p.d = a.d; p.half = a.rot / 2;
+    p.q = a.q; p.k = a.k; p.oq = a.out_q; p.ok = a.out_k;
+    p.ld_q = a.ld_q; p.ld_k = a.ld_k; p.ld_oq = a.ld_oq; p.ld_ok = a.ld_ok;
+    p.positions = a.positions; p.inv_freq = a.inv_freq; p.amp = a.factor; p.inverse = a.inverse;
+    // turned in place, the rest of each head needs no work
+    const bool copy_rest = a.rot < a.d && (a.out_q != a.q || (a.Hkv > 0 && a.out_k != a.k));
+    if (a.dtype == HS_F32) return rope_typed<float>(p, a.interleaved, copy_rest, st);
+    return rope_typed<__nv_bfloat16>(p, a.interleaved, copy_rest, st);
+}
+
+cudaError_t cache_write_launch(const PagedCache &c, int T, int Hkv, int d, int dtype, const void *k, long long ld_k,
+                               const void *v, long long ld_v, const double *inv_freq, int rot, bool interleaved,
+                               float factor, unsigned int *status, cudaStream_t st) {
+    WriteParams p{};
+    p.c = c; p.T = T; p.Hkv = Hkv; p.d = d; p.half = inv_freq ? rot / 2 : 0;
+    p.k = k; p.v = v; p.ld_k = ld_k; p.ld_v = ld_v; p.inv_freq = inv_freq; p.amp = factor;
+    p.interleaved = interleaved; p.status = status;
+    if (dtype == HS_F32) {
+        if (c.dtype == HS_E4M3) return write_go<float, uint8_t, true>(p, st);
+        if (c.dtype == HS_BF16) return write_go<float, __nv_bfloat16, false>(p, st);
+        return write_go<float, float, false>(p, st);
+    }
+    if (c.dtype == HS_E4M3) return write_go<__nv_bfloat16, uint8_t, true>(p, st);
+    if (c.dtype == HS_BF16) return write_go<__nv_bfloat16, __nv_bfloat16, false>(p, st);
+    return write_go<__nv_bfloat16, float, false>(p, st);
+}
+
+cudaError_t cache_read_launch(const PagedCache &c, const int32_t *start, int total, int Hkv, int d, int dtype,
+                              void *k, void *v, unsigned int *status, cudaStream_t st) {
+    ReadParams p{c, start, total, Hkv, d, k, v, status, 1};
+    if (dtype == HS_F32) {
+        if (c.dtype == HS_E4M3) return read_go<__nv_fp8_e4m3, float, true>(p, st);
+        if (c.dtype == HS_BF16) return read_go<__nv_bfloat16, float, false>(p, st);
+        return read_go<float, float, false>(p, st);
+    }
+    if (c.dtype == HS_E4M3) return read_go<__nv_fp8_e4m3, __nv_bfloat16, true>(p, st);
+    if (c.dtype == HS_BF16) return read_go<__nv_bfloat16, __nv_bfloat16, false>(p, st);
+    return read_go<float, __nv_bfloat16, false>(p, st);
+}
+
+}  // namespace hs

@@ -117,4 +117,33 @@ cudaError_t topk_launch(const Shape &s, const float *scores, long long ld, int r
                         int row_count, int topk, int32_t *idx, cudaStream_t st, uint32_t *mask = nullptr,
                         int W = 0, bool *mask_done = nullptr);
 
+// A paged cache and the ragged batch over it (a validated hs_paged_cache):
+// packed rows cu_rows[b] .. cu_rows[b+1]-1 belong to sequence b, whose cache
+// holds kv_len[b] positions in pages block_table[b][0 ..].
+struct PagedCache {
+    const int32_t *cu_rows = nullptr, *kv_len = nullptr, *block_table = nullptr;
+    int B = 0, page_shift = 0, max_pages = 0, num_pages = 0;
+    int dtype = 0;                                   // HS_F32, HS_BF16 or HS_E4M3
+    void *k_pages = nullptr, *v_pages = nullptr;     // [num_pages][page][Hkv][d]
+    uint8_t *k_scale = nullptr, *v_scale = nullptr;  // [num_pages][Hkv][page] (HS_E4M3)
+};
+
+// cache_ops.cu
+struct RopeCall {
+    int T, Hq, Hkv, d, rot, dtype;
+    bool interleaved, inverse;
+    float factor;
+    const void *q, *k;
+    void *out_q, *out_k;
+    long long ld_q, ld_k, ld_oq, ld_ok;              // elements from one token to the next
+    const int32_t *positions;
+    const double *inv_freq;
+};
+cudaError_t rope_launch(const RopeCall &a, cudaStream_t st);
+cudaError_t cache_write_launch(const PagedCache &c, int T, int Hkv, int d, int dtype, const void *k, long long ld_k,
+                               const void *v, long long ld_v, const double *inv_freq, int rot, bool interleaved,
+                               float factor, unsigned int *status, cudaStream_t st);
+cudaError_t cache_read_launch(const PagedCache &c, const int32_t *start, int total, int Hkv, int d, int dtype,
+                              void *k, void *v, unsigned int *status, cudaStream_t st);
+
 }  // namespace hs

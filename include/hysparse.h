@@ -73,7 +73,8 @@ typedef enum {
     HS_ERR_TIMEOUT = 6        /* (device) a bounded wait inside a kernel gave up */
 } hs_status;
 
-typedef enum { HS_F32 = 0, HS_BF16 = 1 } hs_dtype;
+/* HS_E4M3 is a page pool's type only (hs_paged_cache). */
+typedef enum { HS_F32 = 0, HS_BF16 = 1, HS_E4M3 = 2 } hs_dtype;
 
 typedef struct {
     int B, Lq, Lkv, Hq, Hkv, d;
@@ -242,6 +243,87 @@ int hysparse_block_paged(const hs_shape *shape, const int32_t *kv_len, const int
                          int n_sparse, const void *const *q_sparse, const float *const *gate_logit,
                          void *const *out_sparse, int topk, int window, int32_t *idx_out, void *ws,
                          size_t ws_bytes, hs_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Ragged batches and paged caches: the calls below serve prompts and chunks
+ * of sequences of different lengths, packed row after row ([T][H][d], no
+ * padding between sequences), next to the decode calls above, which read the
+ * same pages.  (The pages of the method have no counterpart; this is the
+ * serving side of their prefill / decode split.)
+ *
+ *   - Row strides: ld_x is the number of elements from one packed row of x to
+ *     the next (>= H * d, a multiple of 16 bytes), so q, k and v may be
+ *     slices of one projection's output; each row's [H][d] is contiguous.
+ *   - cu_rows (DEVICE int32, B + 1 entries, ascending): rows cu_rows[b] ..
+ *     cu_rows[b+1]-1 are sequence b's (none when equal).  Rows before
+ *     cu_rows[0] or from cu_rows[B] on belong to no sequence: they are not
+ *     read into any result and their outputs are left as they were.
+ *   - The values of device arrays are checked on the device: an entry that
+ *     would leave the caller's buffers is skipped or clamped and recorded in
+ *     the workspace status word (HS_ERR_INVALID_ARG for lengths and
+ *     positions, HS_ERR_INVALID_INDEX for block table entries), when the call
+ *     has a workspace. */
+
+/* A paged cache and the batch over it.  k_pages and v_pages are pools
+ * [num_pages][page_size][Hkv][d] of cache_dtype; sequence b's position j is
+ * row j % page_size of page block_table[b * max_pages + j / page_size].
+ * page_size is a power of two in [1, 65536]; num_pages * page_size and
+ * max_pages * page_size are below 2^31.
+ * HS_E4M3 pools hold 8-bit floats (4 exponent bits, 3 mantissa bits) with one
+ * scale byte per row and head in k_scale / v_scale [num_pages][Hkv][page_size]:
+ * an element stands for code * 2^(byte - 127).  A power of two makes every
+ * such value a bf16 number exactly. */
+typedef struct {
+    const int32_t *cu_rows;       /* DEVICE [B + 1] */
+    const int32_t *kv_len;        /* DEVICE [B]: positions in each cache, the new rows' among them */
+    const int32_t *block_table;   /* DEVICE [B][max_pages] */
+    int B, page_size, max_pages, num_pages;
+    int cache_dtype;              /* hs_dtype */
+    void *k_pages, *v_pages;
+    uint8_t *k_scale, *v_scale;   /* HS_E4M3 only */
+} hs_paged_cache;
+
+/* Flags of the rotary calls. */
+#define HS_ROPE_INTERLEAVED 1     /* pairs (2i, 2i+1); without it (i, i + rot/2) */
+#define HS_ROPE_INVERSE 2         /* turn back: the transposed rotation, which is the gradient's */
+
+/* Rotary positions: for every packed row t, head and pair i < rot/2, with
+ * angle a = positions[t] * inv_freq[i] (in 64 bits):
+ *   (x, y) -> factor * (x cos a - y sin a, y cos a + x sin a),
+ * elements from rot on are copied.  q has Hq heads and k Hkv (k may be left
+ * out: Hkv = 0).  dtype HS_F32 or HS_BF16; d a multiple of 8 up to 512; rot
+ * even, 2 <= rot <= d; positions DEVICE int32 [T] (any sign), inv_freq DEVICE
+ * double [rot/2].  out_q / out_k may be q / k themselves (same stride), else
+ * they must not overlap the inputs.
+ * Errors: HS_ERR_INVALID_ARG, HS_ERR_UNSUPPORTED, HS_ERR_CUDA. */
+int hysparse_rope(int T, int Hq, int Hkv, int d, int dtype, const void *q, long long ld_q, const void *k,
+                  long long ld_k, const int32_t *positions, const double *inv_freq, int rot, int flags, float factor,
+                  void *out_q, long long ld_oq, void *out_k, long long ld_ok, hs_stream_t stream);
+
+/* Write new keys and values into a paged cache: packed row r of sequence b
+ * (of its n = cu_rows[b+1] - cu_rows[b] new rows) goes to position
+ * kv_len[b] - n + (r - cu_rows[b]).  With inv_freq (else NULL) the keys are
+ * turned as by hysparse_rope at those positions on the way, without a
+ * rounding in between (flags: HS_ROPE_INTERLEAVED or 0).
+ * k, v [T][Hkv][d] of dtype HS_F32 or HS_BF16; d a multiple of 16 up to 256.
+ * HS_E4M3 pools get, per row and head, the smallest power of two 2^e with
+ * max|x| <= 448 * 2^e (2^0 for a row of zeros, e >= -126) as byte e + 127 and
+ * the nearest 8-bit floats (ties to even) of x / 2^e.  Other pool types get x
+ * rounded once.  Two rows of one call must not share a pool row.
+ * ws (nullable) is only used for its status word.
+ * Errors: HS_ERR_INVALID_ARG, HS_ERR_UNSUPPORTED, HS_ERR_CUDA. */
+int hysparse_cache_write(const hs_paged_cache *cache, int T, int Hkv, int d, int dtype, const void *k, long long ld_k,
+                         const void *v, long long ld_v, const double *inv_freq, int rot, int flags, float factor,
+                         void *ws, hs_stream_t stream);
+
+/* Read rows of a paged cache back, widened and packed: row cu_rows[b] + i of
+ * k, v ([total][Hkv][d] of dtype, contiguous) is position start[b] + i of
+ * sequence b (start NULL: from 0 on).  cache->kv_len is not read.  A position
+ * or page outside the cache leaves its output row as it was and is recorded.
+ * ws (nullable) is only used for its status word.
+ * Errors: HS_ERR_INVALID_ARG, HS_ERR_UNSUPPORTED, HS_ERR_CUDA. */
+int hysparse_cache_read(const hs_paged_cache *cache, const int32_t *start, int total, int Hkv, int d, int dtype,
+                        void *k, void *v, void *ws, hs_stream_t stream);
 
 /* Allocation-free variant of hysparse_full_attn_scores (the pages have no
  * counterpart; this is a deployment convenience).  Same computation,

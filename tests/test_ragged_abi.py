@@ -1,0 +1,95 @@
+"""Host-side checks of the ragged-batch calls (no GPU): bad arguments are
+refused with the documented status before anything is launched.  Pointers
+are fake device addresses: argument checking never dereferences them, and
+every call below is refused (or has no rows)."""
+import ctypes
+
+import pytest
+
+from hybrid_sparse_attention_tcgen05_b200 import _lib, build as hs_build
+
+A = 0x7f0000000000
+P = lambda i, off=0: ctypes.c_void_p(A + 0x100000 * i + off)
+BAD, UNS, OK = _lib.HS_ERR_INVALID_ARG, _lib.HS_ERR_UNSUPPORTED, _lib.HS_OK
+
+
+@pytest.fixture(scope="module")
+def L():
+    hs_build.build()
+    return _lib.lib()
+
+
+def cache(**kw):
+    a = dict(cu=P(20), kv=P(21), table=P(22), B=2, page=16, max_pages=8, num_pages=100, dtype=_lib.HS_BF16, k=P(23),
+             v=P(24), ks=None, vs=None)
+    a.update(kw)
+    val = lambda x: x.value if isinstance(x, ctypes.c_void_p) else x
+    return _lib.HsPagedCache(val(a["cu"]), val(a["kv"]), val(a["table"]), a["B"], a["page"], a["max_pages"],
+                             a["num_pages"], a["dtype"], val(a["k"]), val(a["v"]), val(a["ks"]), val(a["vs"]))
+
+
+BAD_CACHES = [(dict(cu=None), BAD), (dict(cu=P(20, 2)), BAD), (dict(table=None), BAD), (dict(table=P(22, 1)), BAD),
+              (dict(B=0), BAD), (dict(page=0), BAD), (dict(page=24), BAD), (dict(page=1 << 17), BAD),
+              (dict(max_pages=0), BAD), (dict(num_pages=0), BAD), (dict(page=1 << 16, num_pages=1 << 15), BAD),
+              (dict(page=1 << 16, max_pages=1 << 15), BAD), (dict(dtype=3), BAD), (dict(dtype=-1), BAD),
+              (dict(k=None), BAD), (dict(v=P(24, 8)), BAD), (dict(dtype=_lib.HS_E4M3), BAD),
+              (dict(dtype=_lib.HS_E4M3, ks=P(25)), BAD)]
+
+
+def test_rope_rejects(L):
+    def f(T=4, Hq=2, Hkv=1, d=64, dt=_lib.HS_F32, q=P(1), ldq=128, k=P(2), ldk=64, pos=P(3), fr=P(4), rot=64, flags=0,
+          factor=1.0, oq=P(5), ldoq=128, ok=P(6), ldok=64):
+        return L.hysparse_rope(T, Hq, Hkv, d, dt, q, ldq, k, ldk, pos, fr, rot, flags, factor, oq, ldoq, ok, ldok, None)
+    assert f(T=0) == OK
+    for kw in (dict(T=-1), dict(Hq=0), dict(Hkv=-1), dict(Hq=5000), dict(dt=2), dict(dt=7), dict(q=None), dict(q=P(1, 8)),
+               dict(k=None), dict(ok=None), dict(ok=P(6, 4)), dict(oq=None), dict(pos=None), dict(pos=P(3, 2)),
+               dict(fr=None), dict(fr=P(4, 4)), dict(rot=0), dict(rot=63), dict(rot=66), dict(rot=-2), dict(flags=4),
+               dict(factor=float("nan")), dict(factor=float("inf")), dict(ldq=127), dict(ldq=129), dict(ldq=0),
+               dict(ldk=60), dict(ldoq=130), dict(ldok=8), dict(oq=P(1), ldoq=132), dict(ok=P(2), ldok=68)):
+        assert f(**kw) == BAD, kw
+    for kw in (dict(d=60, rot=60, ldq=120, ldk=60, ldoq=120, ldok=60), dict(d=520, ldq=1040, ldk=520, ldoq=1040, ldok=520)):
+        assert f(**kw) == UNS, kw
+
+
+def test_cache_write_rejects(L):
+    def f(c=None, T=4, H=2, d=128, dt=_lib.HS_BF16, k=P(1), ldk=256, v=P(2), ldv=256, fr=None, rot=0, flags=0,
+          factor=1.0, ws=None):
+        c = c or cache()
+        return L.hysparse_cache_write(ctypes.byref(c), T, H, d, dt, k, ldk, v, ldv, fr, rot, flags, factor, ws, None)
+    assert f(T=0) == OK
+    for kw, want in BAD_CACHES + [(dict(kv=None), BAD), (dict(kv=P(21, 2)), BAD)]:
+        assert f(c=cache(**kw)) == want, kw
+    for kw in (dict(T=-1), dict(H=0), dict(dt=2), dict(k=None), dict(v=P(2, 8)), dict(ldk=255), dict(ldv=257), dict(ldk=0),
+               dict(fr=P(3, 4), rot=64), dict(fr=P(3), rot=0), dict(fr=P(3), rot=130), dict(fr=P(3), rot=31),
+               dict(fr=P(3), rot=64, factor=float("nan")), dict(flags=2), dict(ws=P(9, 4))):
+        assert f(**kw) == BAD, kw
+    for d in (8, 72, 272):
+        assert f(d=d, ldk=2 * d, ldv=2 * d) == UNS
+    assert L.hysparse_cache_write(None, 4, 2, 128, 1, P(1), 256, P(2), 256, None, 0, 0, 1.0, None, None) == BAD
+
+
+def test_cache_read_rejects(L):
+    def f(c=None, start=None, total=4, H=2, d=128, dt=_lib.HS_BF16, k=P(1), v=P(2), ws=None):
+        c = c or cache(kv=None)
+        return L.hysparse_cache_read(ctypes.byref(c), start, total, H, d, dt, k, v, ws, None)
+    assert f(total=0) == OK
+    for kw, want in BAD_CACHES:
+        assert f(c=cache(**kw)) == want, kw
+    for kw in (dict(total=-1), dict(H=0), dict(dt=2), dict(k=None), dict(v=P(2, 4)), dict(start=P(3, 2)), dict(ws=P(9, 8))):
+        assert f(**kw) == BAD, kw
+    assert f(d=40) == UNS
+    assert L.hysparse_cache_read(None, None, 4, 2, 128, 1, P(1), P(2), None, None) == BAD
+
+
+def test_binding_refuses():
+    """Shapes, types and places that the binding checks before the library does."""
+    import torch
+    import hybrid_sparse_attention_tcgen05_b200 as hs
+    q = torch.zeros(4, 2, 64)
+    with pytest.raises(ValueError):
+        hs.rope(q, torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.float64))       # CPU tensors
+    for kw in (dict(rot_dim=0), dict(rot_dim=3), dict(rot_dim=8, scaling="other"), dict(rot_dim=8, factor=0.5),
+               dict(rot_dim=8, scaling="parts", factor=2.0), dict(rot_dim=2, scaling="base", factor=2.0),
+               dict(rot_dim=8, scaling="bands", original_len=10, slow=2.0, fast=1.0)):
+        with pytest.raises(ValueError):
+            hs.rope_frequencies(**kw, device="cpu")
