@@ -21,6 +21,9 @@ Around the paged caches that ``block_paged`` decodes over (module ``ragged``):
 * ``rope`` (and ``rope_frequencies``) -- rotary positions of q and k.
 * ``cache_write`` / ``cache_read`` -- new rows into the pages, plain or as 8-bit
   floats, and rows back out of them.
+* ``packed_attn`` -- causal attention over whole packed prompts.
+* ``chunk_attn_paged`` -- attention of new tokens (one a sequence or many) over
+  the pages.
 """
 from __future__ import annotations
 
@@ -32,11 +35,13 @@ import torch
 
 from . import _lib
 from ._lib import HysparseError, HsShape
-from .ragged import cache_read, cache_write, rope, rope_frequencies
+from .ragged import (cache_read, cache_write, chunk_attn_paged, packed_attn, ragged_workspace_size, rope,
+                     rope_frequencies)
 
 __all__ = ["shape_of", "workspace_size", "alloc_workspace", "full_attn_scores", "topk",
            "sparse_attn", "block", "block_paged", "workspace_status", "version", "launch_count",
-           "kv_cache_bytes", "rope", "rope_frequencies", "cache_write", "cache_read", "HysparseError", "HsShape"]
+           "kv_cache_bytes", "rope", "rope_frequencies", "cache_write", "cache_read",
+           "packed_attn", "chunk_attn_paged", "ragged_workspace_size", "HysparseError", "HsShape"]
 
 
 def _dtype_code(t: torch.dtype) -> int:

@@ -42,6 +42,9 @@ EXPORTS = (
     "hysparse_rope",
     "hysparse_cache_write",
     "hysparse_cache_read",
+    "hysparse_ragged_workspace_size",
+    "hysparse_packed_attn",
+    "hysparse_chunk_attn_paged",
     "hysparse_workspace_status",
     "hysparse_probe_l2_read",
     "hysparse_launch_count",
@@ -111,6 +114,12 @@ def lib():
     L.hysparse_cache_write.restype = I
     L.hysparse_cache_read.argtypes = [CP, P, I, I, I, I, P, P, P, P]
     L.hysparse_cache_read.restype = I
+    L.hysparse_ragged_workspace_size.argtypes = [I] * 7
+    L.hysparse_ragged_workspace_size.restype = SZ
+    L.hysparse_packed_attn.argtypes = [P, I, I, I, I, I, I, F, P, LL, P, LL, P, LL, P, P, P, SZ, P]
+    L.hysparse_packed_attn.restype = I
+    L.hysparse_chunk_attn_paged.argtypes = [CP, I, I, I, I, I, I, F, P, LL, P, P, P, SZ, P]
+    L.hysparse_chunk_attn_paged.restype = I
     L.hysparse_probe_l2_read.argtypes = [P, SZ, I, I, I, P, P]
     L.hysparse_probe_l2_read.restype = I
     L.hysparse_launch_count.argtypes = []

@@ -146,4 +146,23 @@ cudaError_t cache_write_launch(const PagedCache &c, int T, int Hkv, int d, int d
 cudaError_t cache_read_launch(const PagedCache &c, const int32_t *start, int total, int Hkv, int d, int dtype,
                               void *k, void *v, unsigned int *status, cudaStream_t st);
 
+// ragged_attn_tc.cu: attention over ragged batches (bf16, d = 128)
+struct RaggedCall {
+    PagedCache cache;                 // cu_rows and B always; the rest when paged
+    bool paged;
+    int B, T, Hq, Hkv, max_q, max_len;
+    float scale;
+    const void *q, *k, *v;            // k, v: packed rows (not paged)
+    long long ld_q, ld_k, ld_v;
+    void *out;
+    float *lse;
+};
+struct RaggedPlan {
+    int works = 1, splits = 1, chunk = 1;
+    size_t ml_off = 0, o_off = 0, bytes = 0;
+};
+RaggedPlan ragged_plan(const RaggedCall &a);
+cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, unsigned long long wait_ns,
+                               cudaStream_t st);
+
 }  // namespace hs

@@ -63,6 +63,32 @@ int resolve_cache(const hs_paged_cache *in, bool need_kv_len, int Hkv, int d, Pa
     return HS_OK;
 }
 
+// What both attention calls and the workspace size share.
+int resolve_attn(int B, int T, int Hq, int Hkv, int d, int max_q, int max_len, float scale, RaggedCall *a) {
+    if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq > kMaxHeads || Hq % Hkv != 0) return HS_ERR_INVALID_ARG;
+    if (max_q < 0 || max_len < 0 || !(scale == scale) || isinf(scale)) return HS_ERR_INVALID_ARG;
+    if (d != 128 || Hq / Hkv > 32) return HS_ERR_UNSUPPORTED;
+    a->B = B;
+    a->T = T;
+    a->Hq = Hq;
+    a->Hkv = Hkv;
+    a->max_q = max_q > 0 ? max_q : T;
+    a->max_len = max_len;
+    a->scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
+    return HS_OK;
+}
+
+int run_attn(const RaggedCall &a, void *ws, size_t ws_bytes, hs_stream_t stream) {
+    if (a.T == 0) return HS_OK;
+    if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4) || !row_stride_ok(a.ld_q, a.Hq, 128, HS_BF16))
+        return HS_ERR_INVALID_ARG;
+    if (!aligned(ws, 256)) return HS_ERR_INVALID_ARG;
+    const RaggedPlan pl = ragged_plan(a);
+    if (ws_bytes < pl.bytes) return HS_ERR_WORKSPACE;
+    const cudaError_t e = ragged_attn_launch(a, pl, ws, wait_limit_ns(), (cudaStream_t)stream);
+    return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? HS_OK : HS_ERR_CUDA; }
 
 }  // namespace
@@ -139,6 +165,47 @@ int hysparse_cache_read(const hs_paged_cache *cache, const int32_t *start, int t
     if (!aligned(k, 16) || !aligned(v, 16)) return HS_ERR_INVALID_ARG;
     return cuda_status(cache_read_launch(c, start, total, Hkv, d, dtype, k, v, (unsigned int *)ws,
                                          (cudaStream_t)stream));
+}
+
+size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int max_q, int max_len) {
+    RaggedCall a{};
+    if (resolve_attn(B, T, Hq, Hkv, d, max_q, max_len, 0.f, &a) != HS_OK) return 0;
+    return ragged_plan(a).bytes;
+}
+
+int hysparse_packed_attn(const int32_t *cu_rows, int B, int T, int Hq, int Hkv, int d, int max_len, float scale,
+                         const void *q, long long ld_q, const void *k, long long ld_k, const void *v, long long ld_v,
+                         void *out, float *lse, void *ws, size_t ws_bytes, hs_stream_t stream) {
+    RaggedCall a{};
+    const int rc = resolve_attn(B, T, Hq, Hkv, d, max_len, max_len > 0 ? max_len : T, scale, &a);
+    if (rc != HS_OK) return rc;
+    if (!aligned(cu_rows, 4)) return HS_ERR_INVALID_ARG;
+    if (T > 0 && (!aligned(k, 16) || !aligned(v, 16) || !row_stride_ok(ld_k, Hkv, d, HS_BF16) ||
+                  !row_stride_ok(ld_v, Hkv, d, HS_BF16)))
+        return HS_ERR_INVALID_ARG;
+    a.paged = false;
+    a.cache.cu_rows = cu_rows;
+    a.cache.B = B;
+    a.q = q; a.k = k; a.v = v; a.ld_q = ld_q; a.ld_k = ld_k; a.ld_v = ld_v;
+    a.out = out; a.lse = lse;
+    return run_attn(a, ws, ws_bytes, stream);
+}
+
+int hysparse_chunk_attn_paged(const hs_paged_cache *cache, int T, int Hq, int Hkv, int d, int max_q, int max_len,
+                              float scale, const void *q, long long ld_q, void *out, float *lse, void *ws,
+                              size_t ws_bytes, hs_stream_t stream) {
+    if (cache == nullptr) return HS_ERR_INVALID_ARG;
+    RaggedCall a{};
+    int rc = resolve_attn(cache->B, T, Hq, Hkv, d, max_q, max_len, scale, &a);
+    if (rc != HS_OK) return rc;
+    rc = resolve_cache(cache, true, Hkv, d, &a.cache);
+    if (rc != HS_OK) return rc;
+    if (a.cache.dtype == HS_F32) return HS_ERR_UNSUPPORTED;
+    a.paged = true;
+    if (max_len == 0) a.max_len = cache->max_pages * cache->page_size;
+    a.q = q; a.ld_q = ld_q;
+    a.out = out; a.lse = lse;
+    return run_attn(a, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -19,7 +19,8 @@ import torch
 from . import _lib
 from ._lib import HsPagedCache
 
-__all__ = ["rope", "rope_frequencies", "cache_write", "cache_read"]
+__all__ = ["rope", "rope_frequencies", "cache_write", "cache_read", "packed_attn", "chunk_attn_paged",
+           "ragged_workspace_size"]
 
 _DTYPES = {torch.float32: _lib.HS_F32, torch.bfloat16: _lib.HS_BF16}
 _POOL_DTYPES = {**_DTYPES, torch.float8_e4m3fn: _lib.HS_E4M3}
@@ -264,3 +265,84 @@ def cache_read(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_rows: torch.Tens
     _call(dev, _lib.lib().hysparse_cache_read, "hysparse_cache_read", ctypes.byref(c), _p(start), shape[0], Hkv, d,
           _code(dtype), _p(out_k), _p(out_v), _p(ws))
     return out_k, out_v
+
+
+def ragged_workspace_size(B: int, T: int, Hq: int, Hkv: int, d: int = 128, max_q: int = 0, max_len: int = 0) -> int:
+    """Bytes of workspace of packed_attn (max_q = max_len = the longest prompt) and
+    chunk_attn_paged (most new rows of a sequence; the longest cache)."""
+    n = _lib.lib().hysparse_ragged_workspace_size(B, T, Hq, Hkv, d, max_q, max_len)
+    if n == 0:
+        raise _lib.HysparseError(_lib.HS_ERR_INVALID_ARG, "hysparse_ragged_workspace_size")
+    return int(n)
+
+
+def _attn_buffers(q: torch.Tensor, Hkv: int, B: int, max_q: int, max_len: int, out, lse, ws, dev):
+    T, Hq, d, ld = _rows(q, "q")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _dense(out, "out", q.dtype, (T, Hq, d))
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", torch.float32, (Hq, T))
+    if ws is None:   # scratch for this call only: its status word is not read
+        ws = torch.empty(ragged_workspace_size(B, T, Hq, Hkv, d, max_q, max_len), dtype=torch.uint8, device=dev)
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return T, Hq, d, ld, out, lse, ws
+
+
+def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                max_len: Optional[int] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Causal attention over whole packed prompts (hysparse_packed_attn).
+
+    q [T, Hq, 128], k and v [T, Hkv, 128] bfloat16, cu_seqlens int32 [B + 1]
+    on the device; max_len: the longest prompt (default T).  Returns
+    (out [T, Hq, 128], lse [Hq, T] f32, natural log)."""
+    dev = _device(q, k, v, cu_seqlens, out, lse, ws)
+    Tk, Hkv, dk, ld_k = _rows(k, "k")
+    Tv, Hv, dv, ld_v = _rows(v, "v")
+    if (Tv, Hv, dv) != (Tk, Hkv, dk) or (Tk, dk) != (q.shape[0], q.shape[-1]):
+        raise ValueError("q, k and v disagree on rows, heads or head dim")
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("k and v must be bfloat16")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold B + 1 entries")
+    B = cu_seqlens.numel() - 1
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    longest = Tk if max_len is None else int(max_len)
+    T, Hq, d, ld_q, out, lse, ws = _attn_buffers(q, Hkv, B, longest, longest, out, lse, ws, dev)
+    _call(dev, _lib.lib().hysparse_packed_attn, "hysparse_packed_attn", _p(cu_seqlens), B, T, Hq, Hkv, d, longest,
+          float(scale or 0.0), _p(q), ld_q, _p(k), ld_k, _p(v), ld_v, _p(out), _p(lse), _p(ws),
+          ws.numel() * ws.element_size())
+    return out, lse
+
+
+def chunk_attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torch.Tensor,
+                     kv_len: torch.Tensor, block_table: torch.Tensor, *, max_q: Optional[int] = None,
+                     max_len: Optional[int] = None, k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None):
+    """Attention of new tokens over a paged cache that holds them already
+    (hysparse_chunk_attn_paged).
+
+    q [T, Hq, 128] bfloat16; pages, scales, kv_len and block_table as
+    cache_write takes them (bfloat16 or float8_e4m3fn pools).  max_q: most new
+    rows of a sequence (default T; 1 for a decode step); max_len: the longest
+    cache (default max_pages * page_size; it only plans the work).  Returns
+    (out [T, Hq, 128], lse [Hq, T] f32, natural log)."""
+    dev = _device(q, k_pages, v_pages, cu_seqlens, kv_len, block_table, k_scale, v_scale, out, lse, ws)
+    c, Hkv, dp = _paged(k_pages, v_pages, cu_seqlens, kv_len, block_table, k_scale, v_scale)
+    if dp != q.shape[-1]:
+        raise ValueError("q and the pages disagree on head dim")
+    most = q.shape[0] if max_q is None else int(max_q)
+    longest = c.max_pages * c.page_size if max_len is None else int(max_len)
+    T, Hq, d, ld_q, out, lse, ws = _attn_buffers(q, Hkv, c.B, most, longest, out, lse, ws, dev)
+    _call(dev, _lib.lib().hysparse_chunk_attn_paged, "hysparse_chunk_attn_paged", ctypes.byref(c), T, Hq, Hkv, d, most,
+          longest, float(scale or 0.0), _p(q), ld_q, _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size())
+    return out, lse

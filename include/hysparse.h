@@ -325,6 +325,51 @@ int hysparse_cache_write(const hs_paged_cache *cache, int T, int Hkv, int d, int
 int hysparse_cache_read(const hs_paged_cache *cache, const int32_t *start, int total, int Hkv, int d, int dtype,
                         void *k, void *v, void *ws, hs_stream_t stream);
 
+/* Bytes of workspace that the two attention calls below need for these
+ * arguments (0 for invalid ones): 256 for the status word, and where few rows
+ * face many keys, the partial results of the pieces their keys are split
+ * into.  At most 94 MB.  A workspace belongs to one call at a time:
+ * calls (or replayed graphs) that may overlap on the GPU need one each.
+ * Status word as in hysparse_workspace_size. */
+size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int max_q, int max_len);
+
+/* Causal attention over whole packed prompts: with sequence b's rows
+ * s = cu_rows[b] .. cu_rows[b+1]-1 of q [T][Hq][d], k and v [T][Hkv][d]
+ * (bf16, d = 128, Hq / Hkv <= 32):
+ *   out[t,h] = sum_{s <= j <= t} softmax_j(scale * q[t,h].k[j,h/G]) v[j,h/G]
+ *   lse[h,t] = ln sum_{s <= j <= t} exp(scale * q[t,h].k[j,h/G])
+ * out [T][Hq][d] bf16 and lse [Hq][T] float, contiguous.  scale <= 0 selects
+ * 1/sqrt(d).  max_len: the longest sequence (0: T); a longer one is recorded
+ * as HS_ERR_INVALID_ARG and some of its rows are left out.  Rows of no
+ * sequence are left as they were.  Probabilities are rounded to bf16 before
+ * they meet v; sums are held in fp32.  A wait that gives up
+ * (HS_ERR_TIMEOUT) marks its rows' lse with NaN.
+ * ws: 256-byte aligned, hysparse_ragged_workspace_size(B, T, Hq, Hkv, d,
+ * max_len, max_len) bytes.
+ * Errors: HS_ERR_INVALID_ARG, HS_ERR_UNSUPPORTED, HS_ERR_WORKSPACE, HS_ERR_CUDA. */
+int hysparse_packed_attn(const int32_t *cu_rows, int B, int T, int Hq, int Hkv, int d, int max_len, float scale,
+                         const void *q, long long ld_q, const void *k, long long ld_k, const void *v, long long ld_v,
+                         void *out, float *lse, void *ws, size_t ws_bytes, hs_stream_t stream);
+
+/* Attention of a chunk of new tokens over a paged cache that holds them
+ * already (hysparse_cache_write): sequence b's n = cu_rows[b+1] - cu_rows[b]
+ * rows of q [T][Hq][d] (bf16, d = 128, Hq / Hkv <= 32) are its cache's last
+ * positions; row i sees positions 0 .. kv_len[b] - n + i.  One row a sequence
+ * is a decode step.  out, lse, scale, max_q (most rows of a sequence; 0: T)
+ * as in hysparse_packed_attn; a row that sees nothing (kv_len[b] < n) gets
+ * zeros and lse = -inf.  max_len: the longest cache (0: max_pages *
+ * page_size); it only plans the work, longer ones are still right.
+ * Pools of HS_BF16 or HS_E4M3.  Only the table entries that cover
+ * positions 0 .. kv_len[b]-1 are read, and nothing that lies behind
+ * kv_len[b] in the last page reaches a result (NaN included).  A page outside
+ * the pool drops its keys.  ws: 256-byte aligned,
+ * hysparse_ragged_workspace_size(B, T, Hq, Hkv, d, max_q, the longest cache)
+ * bytes.
+ * Errors: as hysparse_packed_attn; HS_ERR_UNSUPPORTED for fp32 pools. */
+int hysparse_chunk_attn_paged(const hs_paged_cache *cache, int T, int Hq, int Hkv, int d, int max_q, int max_len,
+                              float scale, const void *q, long long ld_q, void *out, float *lse, void *ws,
+                              size_t ws_bytes, hs_stream_t stream);
+
 /* Allocation-free variant of hysparse_full_attn_scores (the pages have no
  * counterpart; this is a deployment convenience).  Same computation,
  * arguments, layouts and errors, but no workspace: its scratch lives in a

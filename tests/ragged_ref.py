@@ -52,28 +52,43 @@ def rows_of(pages, table, first, last, scale=None):
 
 
 def attend(q, k, v, scale, dropped=()):
-    """q [n, Hq, d] at the last n of the m positions of k, v [m, Hkv, d]: (out, lse [Hq, n]) in 64
-    bits; a row that sees nothing gives zeros and -inf.  dropped: positions that are not there."""
+    """q [n, Hq, d] at the last n of the m positions of k, v [m, Hkv, d]: (out, lse [Hq, n],
+    sum_j p_j |v_j|) in 64 bits; a row that sees nothing gives zeros and -inf.  dropped: positions
+    that are not there."""
     n, Hq, d = q.shape
     m, Hkv = k.shape[:2]
     out = torch.zeros(n, Hq, d, dtype=torch.float64)
+    size = torch.zeros(n, Hq, d, dtype=torch.float64)
     lse = torch.full((Hq, n), -math.inf, dtype=torch.float64)
-    keep = torch.ones(m, dtype=torch.bool)
-    for j in dropped:
-        keep[j] = False
-    for i in range(n):
-        pos = m - n + i
-        if pos < 0:
-            continue
-        see = keep[:pos + 1].nonzero()[:, 0]
-        if see.numel() == 0:
-            continue
-        for h in range(Hq):
-            g = h // (Hq // Hkv)
-            s = (k[see, g].double() @ q[i, h].double()) * scale
-            lse[h, i] = torch.logsumexp(s, 0)
-            out[i, h] = torch.exp(s - lse[h, i]) @ v[see, g].double()
-    return out, lse
+    if n == 0 or m == 0:
+        return out, lse, size
+    see = torch.arange(m)[None] <= torch.arange(m - n, m)[:, None]
+    see[:, list(dropped)] = False
+    for h in range(Hq):
+        g = h // (Hq // Hkv)
+        s = (q[:, h].double() @ k[:, g].double().t()) * scale
+        s = s.masked_fill(~see, -math.inf)
+        lse[h] = torch.logsumexp(s, 1)
+        p = torch.exp(s - lse[h].clamp(min=-1e300)[:, None])
+        out[:, h] = p @ v[:, g].double()
+        size[:, h] = p @ v[:, g].double().abs()
+    return out, lse, size
+
+
+def check_attend(name, out, lse, want, slack=0.0):
+    """out, lse of one sequence's rows against attend()'s.  The probabilities are rounded to bf16 before
+    they meet v (2^-8 of each term p |v|), the result to bf16 (2^-8 of it); a score is a sum of 128
+    products in fp32, off by at most 128 * 2^-24 * sum |q k| * scale, which for entries of size ~1 is
+    under 1e-4, and moves each probability by that relative amount (twice: its own and the sum's)."""
+    o, l, size = want
+    tol = (2.0 ** -8 + 2e-4 + slack) * size + 2.0 ** -8 * o.abs() + 1e-30
+    err = (out.double().cpu() - o).abs()
+    assert bool(torch.isfinite(out.float()).all()), f"{name}: not finite"
+    assert bool((err <= tol).all()), f"{name}: off by {float((err - tol).max())} past the bound, error {float(err.max())}"
+    none = torch.isinf(l)
+    assert torch.equal(torch.isinf(lse.cpu()) & (lse.cpu() < 0), none), f"{name}: rows that see nothing"
+    e = (lse.double().cpu() - l)[~none].abs()
+    assert e.numel() == 0 or float(e.max()) <= 1e-4 + slack, f"{name}: lse off by {float(e.max())}"
 
 
 def make_table(gen, need, extra=2, first=0):

@@ -93,3 +93,53 @@ def test_binding_refuses():
                dict(rot_dim=8, scaling="bands", original_len=10, slow=2.0, fast=1.0)):
         with pytest.raises(ValueError):
             hs.rope_frequencies(**kw, device="cpu")
+
+
+def test_ragged_workspace_size(L):
+    f = L.hysparse_ragged_workspace_size
+    assert f(1, 0, 8, 2, 128, 0, 0) == 256 and f(4, 100000, 32, 8, 128, 100000, 100000) == 256   # enough rows: no pieces
+    few = f(1, 1, 8, 2, 128, 1, 32768)
+    assert few > 256 and few % 256 == 0                           # one row, many keys: partial results
+    for a in ((1, 1, 8, 2, 128, 1, 1 << 24), (64, 64, 32, 8, 128, 1, 32768), (3, 700, 64, 4, 128, 300, 1 << 20),
+              (1, 5000, 128, 1, 128, 5000, 1 << 20)):
+        n = f(*a) if a[2] // a[3] <= 32 else 256
+        assert 256 <= n <= 94 << 20
+    for bad in ((0, 1, 8, 2, 128, 1, 1), (1, -1, 8, 2, 128, 1, 1), (1, 1, 0, 2, 128, 1, 1), (1, 1, 8, 3, 128, 1, 1),
+                (1, 1, 8, 0, 128, 1, 1), (1, 1, 8, 2, 64, 1, 1), (1, 1, 33, 1, 128, 1, 1), (1, 1, 8, 2, 128, -1, 1),
+                (1, 1, 8, 2, 128, 1, -1)):
+        assert f(*bad) == 0, bad
+
+
+def test_packed_attn_rejects(L):
+    def f(cu=P(1), B=2, T=64, Hq=8, Hkv=2, d=128, max_len=0, scale=0.0, q=P(2), ldq=1024, k=P(3), ldk=256, v=P(4), ldv=256,
+          out=P(5), lse=P(6), ws=P(7), wsb=1 << 30):
+        return L.hysparse_packed_attn(cu, B, T, Hq, Hkv, d, max_len, scale, q, ldq, k, ldk, v, ldv, out, lse, ws, wsb, None)
+    assert f(T=0) == OK
+    for kw in (dict(cu=None), dict(cu=P(1, 2)), dict(B=0), dict(T=-1), dict(Hq=0), dict(Hkv=3), dict(max_len=-1),
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(q=P(2, 8)), dict(k=None),
+               dict(v=P(4, 2)), dict(ldq=1023), dict(ldq=1028), dict(ldk=0), dict(ldv=260), dict(out=None),
+               dict(out=P(5, 8)), dict(lse=None), dict(lse=P(6, 2)), dict(ws=None), dict(ws=P(7, 16))):
+        assert f(**kw) == BAD, kw
+    assert f(d=64) == UNS and f(Hq=66, Hkv=2, ldq=66 * 128) == UNS
+    assert f(wsb=255) == _lib.HS_ERR_WORKSPACE
+    need = L.hysparse_ragged_workspace_size(2, 64, 8, 2, 128, 4096, 4096)
+    assert need > 256 and f(max_len=4096, wsb=need - 1) == _lib.HS_ERR_WORKSPACE
+
+
+def test_chunk_attn_paged_rejects(L):
+    def f(c=None, T=64, Hq=8, Hkv=2, d=128, max_q=0, max_len=0, scale=0.0, q=P(2), ldq=1024, out=P(5), lse=P(6), ws=P(7),
+          wsb=1 << 30):
+        c = c or cache()
+        return L.hysparse_chunk_attn_paged(ctypes.byref(c), T, Hq, Hkv, d, max_q, max_len, scale, q, ldq, out, lse, ws, wsb,
+                                           None)
+    assert f(T=0) == OK
+    for kw, want in BAD_CACHES + [(dict(kv=None), BAD), (dict(kv=P(21, 2)), BAD), (dict(dtype=_lib.HS_F32), UNS)]:
+        assert f(c=cache(**kw)) == want, kw
+    for kw in (dict(T=-1), dict(Hq=0), dict(Hkv=3), dict(max_q=-1), dict(max_len=-1), dict(scale=float("nan")), dict(q=None),
+               dict(q=P(2, 4)), dict(ldq=1000), dict(ldq=1028), dict(out=None), dict(out=P(5, 8)), dict(lse=P(6, 1)),
+               dict(ws=None), dict(ws=P(7, 128))):
+        assert f(**kw) == BAD, kw
+    assert f(d=64) == UNS and f(Hq=66, ldq=66 * 128) == UNS
+    need = L.hysparse_ragged_workspace_size(2, 64, 8, 2, 128, 64, 128)
+    assert f(max_q=64, wsb=need - 1) == _lib.HS_ERR_WORKSPACE
+    assert L.hysparse_chunk_attn_paged(None, 64, 8, 2, 128, 0, 0, 0.0, P(2), 1024, P(5), P(6), P(7), 1 << 30, None) == BAD
