@@ -347,12 +347,6 @@ __device__ __forceinline__ void widen16(const __nv_fp8_e4m3 *p, float scale, flo
     }
 }
 
-// A scale byte's power of two.  Byte 0 would be 2^-127 (not a normal float)
-// and is never written here; it reads as that all the same.
-__device__ __forceinline__ float scale_of_byte(int byte) {
-    return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)byte << 23);
-}
-
 template <typename TC, typename TO, bool Q8>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p) {
     __shared__ long long slot[kReadTokens];

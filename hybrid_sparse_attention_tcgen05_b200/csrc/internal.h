@@ -158,10 +158,13 @@ struct RaggedCall {
     float *lse;
 };
 struct RaggedPlan {
-    int works = 1, splits = 1, chunk = 1;
+    bool few_rows = false;            // the warp-MMA kernel (ragged_rows_mma.cu)
+    int works = 1, tiles = 1, tile_rows = 16, splits = 1, chunk = 1;
     size_t ml_off = 0, o_off = 0, bytes = 0;
 };
 RaggedPlan ragged_plan(const RaggedCall &a);
+// ragged_rows_mma.cu: at most pl.tile_rows x pl.tiles rows a sequence and KV head, paged
+cudaError_t ragged_rows_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, cudaStream_t st);
 cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, unsigned long long wait_ns,
                                cudaStream_t st);
 

@@ -69,6 +69,12 @@ __device__ __forceinline__ size_t scale_index(const PagedCache &c, long long row
     return ((size_t)(page * Hkv + h) << c.page_shift) + (size_t)(row & ((1ll << c.page_shift) - 1));
 }
 
+// A scale byte's power of two.  Byte 0 would be 2^-127 (not a normal float)
+// and is never written here; it reads as that all the same.
+__device__ __forceinline__ float scale_of_byte(int byte) {
+    return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)byte << 23);
+}
+
 // cos and sin of pos * freq, times `amp`, each rounded once to fp32.  The
 // angle is held in 64 bits: in fp32 a position near a million would be off by
 // 0.06 rad.  It is brought into [-pi, pi] by subtracting whole turns (2 pi as

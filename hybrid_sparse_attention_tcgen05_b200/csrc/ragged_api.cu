@@ -45,7 +45,7 @@ int resolve_cache(const hs_paged_cache *in, bool need_kv_len, int Hkv, int d, Pa
     if ((long long)c.num_pages * ps > 0x7fffffffLL) return HS_ERR_INVALID_ARG;   // pool rows in int32
     if (c.cache_dtype != HS_F32 && c.cache_dtype != HS_BF16 && c.cache_dtype != HS_E4M3) return HS_ERR_INVALID_ARG;
     if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16)) return HS_ERR_INVALID_ARG;
-    if (c.cache_dtype == HS_E4M3 && (c.k_scale == nullptr || c.v_scale == nullptr)) return HS_ERR_INVALID_ARG;
+    if (c.cache_dtype == HS_E4M3 && (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4))) return HS_ERR_INVALID_ARG;
     if (Hkv < 1 || Hkv > kMaxHeads) return HS_ERR_INVALID_ARG;
     if (d < 16 || d > 256 || d % 16 != 0) return HS_ERR_UNSUPPORTED;
     out->cu_rows = c.cu_rows;
@@ -170,7 +170,14 @@ int hysparse_cache_read(const hs_paged_cache *cache, const int32_t *start, int t
 size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int max_q, int max_len) {
     RaggedCall a{};
     if (resolve_attn(B, T, Hq, Hkv, d, max_q, max_len, 0.f, &a) != HS_OK) return 0;
-    return ragged_plan(a).bytes;
+    size_t n = ragged_plan(a).bytes;   // whichever call and pool it is for
+    for (int dtype : {(int)HS_BF16, (int)HS_E4M3}) {
+        a.paged = true;
+        a.cache.dtype = dtype;
+        const size_t m = ragged_plan(a).bytes;
+        n = n > m ? n : m;
+    }
+    return n;
 }
 
 int hysparse_packed_attn(const int32_t *cu_rows, int B, int T, int Hq, int Hkv, int d, int max_len, float scale,

@@ -870,6 +870,11 @@ cudaError_t prepare() {
 }
 
 constexpr int kSms = 148;
+constexpr int kMaxSplits = 64;
+constexpr int kFewRows = 16;               // rows (new tokens x group) a sequence up to which the warp-MMA kernel runs
+constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an SM holds (bf16, 8-bit caches)
+constexpr int kFewRowsFixed = 8;           // what a piece costs besides its keys, in 16-key blocks
+constexpr int kFewRowsMinChunk = 4;        // fewest 16-key blocks in a piece (one for each warp)
 constexpr size_t kMaxPartRows = 180000;    // rows of partial results: 520 bytes each
 
 // Work items of a batch (an upper bound from what the host knows).
@@ -878,6 +883,22 @@ long long work_bound(const RaggedCall &a) {
     const long long by_rows = a.T / qt + a.B;
     const long long by_len = (long long)a.B * ((std::min<long long>(a.max_q, a.T) + qt - 1) / qt);
     return std::max<long long>(1, std::min(by_rows, by_len));
+}
+
+cudaError_t combine_launch(const RaggedParams &p, cudaStream_t st) {
+    if (p.splits == 1) return cudaSuccess;
+    const long long rows = (long long)p.T * p.Hq;
+    if ((rows + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidValue;
+    ragged_combine<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// Workspace layout: status word, (max, sum) and O of every piece of every row.
+void plan_bytes(size_t rows, RaggedPlan *pl) {
+    pl->ml_off = kStatusBytes;
+    pl->o_off = align_up(pl->ml_off + (pl->splits > 1 ? pl->splits * rows * sizeof(float2) : 0), 256);
+    pl->bytes = align_up(pl->o_off + (pl->splits > 1 ? pl->splits * rows * 128 * sizeof(float) : 0), 256);
 }
 
 }  // namespace
@@ -890,12 +911,47 @@ long long work_bound(const RaggedCall &a) {
 RaggedPlan ragged_plan(const RaggedCall &a) {
     using namespace tc;
     RaggedPlan pl;
+    const size_t rows = (size_t)a.T * a.Hq;
+    const int G = a.Hq / a.Hkv;
+    const long long row_most = (long long)std::max(1, std::min(a.max_q, a.T)) * G;   // rows of a sequence, at most
+    if (a.paged && row_most <= kFewRows) {
+        // few rows a sequence: 8- or 16-row tiles on the warp MMAs, pieces of 16-key blocks
+        pl.few_rows = true;
+        pl.tile_rows = row_most <= 8 ? 8 : 16;
+        pl.tiles = (int)((row_most + pl.tile_rows - 1) / pl.tile_rows);
+        const long long items = (long long)a.B * pl.tiles * a.Hkv;
+        const long long blocks = std::max<long long>(1, (a.max_len + 15) / 16);
+        // a piece costs about kFewRowsFixed blocks to start and end, the join of pieces
+        // as much; of the splits within 3 % of the cheapest the finest, because
+        // the caches' real lengths differ and small pieces even them out
+        const long long slots = (long long)kSms * (a.cache.dtype == HS_E4M3 ? kFewRowsCtas8 : kFewRowsCtas16);
+        auto cost = [&](long long s) {
+            const long long chunk = (blocks + s - 1) / s;
+            return (items * s + slots - 1) / slots * (chunk + kFewRowsFixed) + (s > 1 ? kFewRowsFixed : 0);
+        };
+        long long most = std::min<long long>(std::max<long long>(blocks / kFewRowsMinChunk, 1), kMaxSplits);
+        if (rows > 0) most = std::max<long long>(1, std::min<long long>(most, (long long)(kMaxPartRows / rows)));
+        // the finest split of each number of waves (a cheaper one there is none)
+        long long best = cost(1), s = 1;
+        for (int pass = 0; pass < 2; ++pass)
+            for (long long w = 1, t = 0; w <= 32 && t < most; ++w) {
+                t = std::min(most, w * slots / items);
+                if (t < 1) continue;
+                const long long ct = cost(t);
+                if (pass == 0) best = std::min(best, ct);
+                else if (ct * 100 <= best * 103) s = t;
+            }
+        pl.chunk = (int)((blocks + s - 1) / s);
+        pl.splits = (int)((blocks + pl.chunk - 1) / pl.chunk);
+        if (pl.splits == 1) pl.chunk = 0x7fffffff / 16;
+        plan_bytes(rows, &pl);
+        return pl;
+    }
     const long long works = work_bound(a) * a.Hkv;
     const long long tiles = std::max<long long>(1, (a.max_len + BN - 1) / BN);
     pl.works = (int)std::min<long long>(work_bound(a), 0x7fffffff);
-    const size_t rows = (size_t)a.T * a.Hq;
     long long best = -1;
-    for (long long s = 1; s <= std::min<long long>(tiles, 64); ++s) {
+    for (long long s = 1; s <= std::min<long long>(tiles, kMaxSplits); ++s) {
         if (s > 1 && (works * s > 8 * kSms || rows * s > kMaxPartRows)) break;
         const long long chunk = (tiles + s - 1) / s;
         const long long waves = (works * s + kSms - 1) / kSms;
@@ -907,15 +963,14 @@ RaggedPlan ragged_plan(const RaggedCall &a) {
         }
     }
     if (pl.splits == 1) pl.chunk = 0x7fffffff / BN;      // lengths past max_len still run, in one piece
-    pl.ml_off = kStatusBytes;
-    pl.o_off = align_up(pl.ml_off + (pl.splits > 1 ? pl.splits * rows * sizeof(float2) : 0), 256);
-    pl.bytes = align_up(pl.o_off + (pl.splits > 1 ? pl.splits * rows * 128 * sizeof(float) : 0), 256);
+    plan_bytes(rows, &pl);
     return pl;
 }
 
 cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, unsigned long long wait_ns,
                                cudaStream_t st) {
     using namespace tc;
+    cudaError_t e = cudaSuccess;
     RaggedParams p{};
     p.c = a.cache;
     p.paged = a.paged;
@@ -932,6 +987,10 @@ cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *
         p.part_ml = reinterpret_cast<float2 *>((char *)ws + pl.ml_off);
         p.part_o = reinterpret_cast<float *>((char *)ws + pl.o_off);
     }
+    if (pl.few_rows) {
+        e = ragged_rows_launch(a, pl, ws, st);
+        return e == cudaSuccess ? combine_launch(p, st) : e;
+    }
     CUtensorMap mq, mk, mv;
     if (!map_rows(&mq, a.q, a.Hq, a.T, a.ld_q, p.G, p.tpt)) return cudaErrorInvalidValue;
     if (a.paged) {
@@ -945,18 +1004,13 @@ cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *
     }
     const long long blocks = (long long)p.works * p.splits * p.Hkv;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    cudaError_t e = f8 ? prepare<true>() : prepare<false>();
+    e = f8 ? prepare<true>() : prepare<false>();
     if (e != cudaSuccess) return e;
     if (f8) ragged_attn_tc<true><<<(unsigned)blocks, Ring<true>::threads, kRaggedSmem, st>>>(mq, mk, mv, p);
     else ragged_attn_tc<false><<<(unsigned)blocks, Ring<false>::threads, kRaggedSmem, st>>>(mq, mk, mv, p);
     count_launch();
     e = cudaGetLastError();
-    if (e != cudaSuccess || pl.splits == 1) return e;
-    const long long rows = (long long)a.T * a.Hq;
-    if ((rows + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidValue;
-    ragged_combine<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
-    count_launch();
-    return cudaGetLastError();
+    return e == cudaSuccess ? combine_launch(p, st) : e;
 }
 
 }  // namespace hs

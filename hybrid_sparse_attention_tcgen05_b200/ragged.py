@@ -22,6 +22,11 @@ from ._lib import HsPagedCache
 __all__ = ["rope", "rope_frequencies", "cache_write", "cache_read", "packed_attn", "chunk_attn_paged",
            "ragged_workspace_size"]
 
+# what torch.cuda.current_device() and current_stream(dev).cuda_stream return,
+# without the objects they make on the way (two microseconds a call)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 _DTYPES = {torch.float32: _lib.HS_F32, torch.bfloat16: _lib.HS_BF16}
 _POOL_DTYPES = {**_DTYPES, torch.float8_e4m3fn: _lib.HS_E4M3}
 
@@ -33,17 +38,18 @@ def _code(t: torch.dtype, pool: bool = False) -> int:
     return code
 
 
-def _device(*ts: Optional[torch.Tensor]) -> torch.device:
-    dev = None
+def _device(*ts: Optional[torch.Tensor]) -> int:
+    """The index of the one CUDA device that all the tensors are on."""
+    dev = -2
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("hysparse runs on CUDA tensors only (no CPU path)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("all tensors must be on the same device")
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    raise ValueError("hysparse runs on CUDA tensors only (no CPU path)")
+                if dev >= 0:
+                    raise ValueError("all tensors must be on the same device")
+                dev = i
     return dev
 
 
@@ -56,8 +62,8 @@ def _rows(t: torch.Tensor, what: str) -> Tuple[int, int, int, int]:
     if t.dim() != 3:
         raise ValueError(f"{what} must be [T, H, d]")
     T, H, d = t.shape
-    ld = t.stride(0)
-    if T > 0 and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+    ld, sh, sd = t.stride()
+    if T > 0 and ((d > 1 and sd != 1) or (H > 1 and sh != d)):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     return T, H, d, (ld if T > 1 else H * d)
 
@@ -67,19 +73,19 @@ def _dense(t: Optional[torch.Tensor], what: str, dtype=None, shape=None) -> None
         return
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
 
 
-def _call(dev: torch.device, fn, what: str, *args) -> None:
+def _call(dev: int, fn, what: str, *args) -> None:
     """The library call on the tensors' device and that device's current stream."""
-    if dev.index is not None and dev.index != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+            st = fn(*args, _raw_stream(dev))
     else:
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+        st = fn(*args, _raw_stream(dev))
     if st != _lib.HS_OK:
         _lib.check(st, what)
 
@@ -161,17 +167,17 @@ def rope(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, k:
     dev = _device(q, positions, inv_freq, k, out, out_k)
     T, Hq, d, ld_q = _rows(q, "q")
     rot = _inv_freq(inv_freq, d)
-    if positions.dtype != torch.int32 or tuple(positions.shape) != (T,) or not positions.is_contiguous():
+    if positions.dtype != torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
         raise TypeError("positions must be a contiguous int32 vector, one per row")
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        out = q.new_empty((T, Hq, d))
     Hkv, ld_k, ld_ok = 0, 0, 0
     if k is not None:
         Tk, Hkv, dk, ld_k = _rows(k, "k")
         if Tk != T or dk != d or k.dtype != q.dtype:
             raise ValueError("q and k disagree on rows, head dim or dtype")
         if out_k is None:
-            out_k = torch.empty((T, Hkv, d), dtype=k.dtype, device=dev)
+            out_k = k.new_empty((T, Hkv, d))
         if out_k.shape != k.shape or out_k.dtype != k.dtype:
             raise ValueError("out_k must be like k")
         ld_ok = _rows(out_k, "out_k")[3]
@@ -256,9 +262,9 @@ def cache_read(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_rows: torch.Tens
     _dense(start, "start", torch.int32, (c.B,))
     shape = (int(total), Hkv, d)
     if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=dev)
+        out_k = k_pages.new_empty(shape, dtype=dtype)
     if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=dev)
+        out_v = k_pages.new_empty(shape, dtype=dtype)
     _dense(out_k, "out_k", dtype, shape)
     _dense(out_v, "out_v", dtype, shape)
     _status_ws(ws)
@@ -276,20 +282,20 @@ def ragged_workspace_size(B: int, T: int, Hq: int, Hkv: int, d: int = 128, max_q
     return int(n)
 
 
-def _attn_buffers(q: torch.Tensor, Hkv: int, B: int, max_q: int, max_len: int, out, lse, ws, dev):
+def _attn_buffers(q: torch.Tensor, Hkv: int, B: int, max_q: int, max_len: int, out, lse, ws):
     T, Hq, d, ld = _rows(q, "q")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        out = q.new_empty((T, Hq, d))
     else:
         _dense(out, "out", q.dtype, (T, Hq, d))
     if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        lse = q.new_empty((Hq, T), dtype=torch.float32)
     else:
         _dense(lse, "lse", torch.float32, (Hq, T))
     if ws is None:   # scratch for this call only: its status word is not read
-        ws = torch.empty(ragged_workspace_size(B, T, Hq, Hkv, d, max_q, max_len), dtype=torch.uint8, device=dev)
+        ws = q.new_empty(ragged_workspace_size(B, T, Hq, Hkv, d, max_q, max_len), dtype=torch.uint8)
     elif not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
     return T, Hq, d, ld, out, lse, ws
@@ -315,7 +321,7 @@ def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     B = cu_seqlens.numel() - 1
     _dense(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
     longest = Tk if max_len is None else int(max_len)
-    T, Hq, d, ld_q, out, lse, ws = _attn_buffers(q, Hkv, B, longest, longest, out, lse, ws, dev)
+    T, Hq, d, ld_q, out, lse, ws = _attn_buffers(q, Hkv, B, longest, longest, out, lse, ws)
     _call(dev, _lib.lib().hysparse_packed_attn, "hysparse_packed_attn", _p(cu_seqlens), B, T, Hq, Hkv, d, longest,
           float(scale or 0.0), _p(q), ld_q, _p(k), ld_k, _p(v), ld_v, _p(out), _p(lse), _p(ws),
           ws.numel() * ws.element_size())
@@ -342,7 +348,7 @@ def chunk_attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         raise ValueError("q and the pages disagree on head dim")
     most = q.shape[0] if max_q is None else int(max_q)
     longest = c.max_pages * c.page_size if max_len is None else int(max_len)
-    T, Hq, d, ld_q, out, lse, ws = _attn_buffers(q, Hkv, c.B, most, longest, out, lse, ws, dev)
+    T, Hq, d, ld_q, out, lse, ws = _attn_buffers(q, Hkv, c.B, most, longest, out, lse, ws)
     _call(dev, _lib.lib().hysparse_chunk_attn_paged, "hysparse_chunk_attn_paged", ctypes.byref(c), T, Hq, Hkv, d, most,
           longest, float(scale or 0.0), _p(q), ld_q, _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size())
     return out, lse

@@ -178,6 +178,67 @@ def test_chunk_matches_definition(hq, hkv, P, pool):
 
 
 @pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("P", [64, 16, 8, 4, 2, 1])
+@pytest.mark.parametrize("hq,hkv,most", [(8, 2, 1), (3, 1, 2), (16, 1, 1), (5, 5, 3), (7, 1, 2), (32, 8, 4), (64, 2, 1),
+                                         (8, 2, 16), (12, 4, 7)])
+def test_chunk_few_rows_match_definition(hq, hkv, most, P, pool):
+    """Decode steps and short chunks: few rows a sequence, one and several 16-row tiles of them, caches
+    that end before, at and behind a 16-key block, empty sequences and caches shorter than the chunk."""
+    gen = torch.Generator().manual_seed(P * 100 + hq + most)
+    new = [most, 0, 1, most, 1, min(2, most), most]
+    kv = [most, 5, 16, 33 + most, 17, 1, 300 + most]
+    table, got = _paged(gen, kv, P, hkv, pool)
+    T = sum(new) + 2
+    q = torch.randn(T, hq, 128, generator=gen).to(BF)
+    cu = ref.cu_of(new) + 1
+    out = torch.full((T, hq, 128), 5.0, dtype=BF, device=DEV)
+    lse = torch.full((hq, T), 5.0, device=DEV)
+    ws = torch.zeros(hs.ragged_workspace_size(len(new), T, hq, hkv, 128, most, 4096), dtype=torch.uint8, device=DEV)
+    _chunk(q, got, cu, kv, table, max_q=most, max_len=4096, out=out, lse=lse, ws=ws)
+    assert hs.workspace_status(ws) == _lib.HS_OK
+    _check_all(f"P {P}", q, got, cu, new, out, lse)
+    assert bool((out[0] == 5).all()) and bool((out[-1] == 5).all()) and bool((lse[:, [0, T - 1]] == 5).all())
+    assert bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("new", [[1, 1], [90, 1]])
+def test_chunk_8bit_scales_far_apart(new):
+    """Scales over the whole range in one cache: keys whose scores vanish beside others', values a
+    million times larger than their neighbours' on keys that count and on keys that do not.  Queries
+    from 2^-30 to 2^30 of the usual size meet keys scaled the other way."""
+    gen = torch.Generator().manual_seed(5)
+    hq, hkv, P, old = 4, 2, 16, [400, 333]
+    kv = [a + b for a, b in zip(new, old)]
+    table, pages = ref.make_table(gen, [-(-n // P) for n in kv])
+    pools = {}
+    for name in ("k", "v"):
+        codes = torch.randn(pages, P, hkv, 128, generator=gen).mul_(8).to(torch.float8_e4m3fn)
+        byte = torch.full((pages, hkv, P), 124, dtype=torch.uint8)
+        if name == "v":
+            pick = torch.randint(0, 60, byte.shape, generator=gen)
+            byte[pick == 0] = 144                  # 2^20 above
+            byte[pick == 1] = 100
+            byte[pick == 2] = 1
+        else:
+            pick = torch.randint(0, 60, byte.shape, generator=gen)
+            byte[pick == 0] = 1
+            byte[pick == 1] = 90
+        pools[name] = (codes, byte)
+    for shift in (0, -30, 30):
+        q = (torch.randn(sum(new), hq, 128, generator=gen) * 2.0 ** shift).to(BF)
+        got, rows = {}, {}
+        for name, (codes, byte) in pools.items():
+            b = (byte.int() - shift).clamp(1, 254).to(torch.uint8) if name == "k" else byte
+            got[name] = (codes.to(DEV), b.to(DEV), [ref.rows_of(codes, table[i], 0, n, b) for i, n in enumerate(kv)])
+        cu = ref.cu_of(new)
+        out, lse = _chunk(q, got, cu, kv, table, max_q=max(new), max_len=max(kv))
+        for b, n in enumerate(new):
+            part = slice(int(cu[b]), int(cu[b]) + n)
+            ref.check_attend(f"shift {shift} seq {b}", out[part], lse[:, part],
+                             ref.attend(q[part], got["k"][2][b], got["v"][2][b], SCALE), slack=1e-4)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
 @pytest.mark.parametrize("new,old", [([1], [5000]), ([1, 1, 1], [3000, 0, 40]), ([40], [4100]), ([300, 2], [1500, 3500]),
                                      ([1], [16383])])
 def test_chunk_long_caches_split(new, old, pool):
