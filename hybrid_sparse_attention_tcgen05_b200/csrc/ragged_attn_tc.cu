@@ -14,16 +14,19 @@
 // K/V tile is loaded once for 256 rows.  When only the first tile has tokens
 // (decode, short chunks) both softmax warpgroups share it and take the key
 // tiles in turn ("solo"); their results are joined at the end.
-// A piece of at most `chunk` key tiles is one CTA's; sequences with more keys
-// are split over several CTAs, whose partial results a second kernel joins.
+// A piece of at most `chunk` key tiles is one item; sequences with more keys
+// are split over several items, whose partial results a second kernel joins.
 //
-// CTA (warps):
+// One CTA per SM runs through its share of the items (longest first, dealt
+// forth and back), so that an item's loads and first products run under the
+// softmax and the stores of the one before.  CTA (warps):
 //   0-3, 4-7  softmax warpgroups, thread = row
 //   8         TMA producer (Q once; K and V tiles, or the pages that make one
 //             up, in the order the MMAs consume them)
 //   9         MMA issuer (one thread)
 //   10        zeroes the value rows behind a sequence's end (whatever lies
 //             there, NaN included, would reach the output as 0 * NaN)
+//   11        finds the items, two ahead
 //   12-15     8-bit caches only: widen staged rows to bf16 tiles.  A code
 //             times a power of two is a bf16 number, so nothing is rounded.
 // TMEM (512 columns): S0 | S1 | O0 | O1.  P overwrites its S tile (64 of 128
@@ -31,9 +34,11 @@
 // memory, Q K^T and P V of 128 keys read 128 bytes a clock, all that shared
 // memory has, and writing P there too would add a quarter; from TMEM the P V
 // products read V only.  The two tiles alternate on the tensor cores: one's
-// softmax runs under the other's products.
+// softmax runs under the other's products.  P is handed over in two halves,
+// so that the first half's product runs under the second half's exponentials.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -52,11 +57,12 @@ namespace {
 constexpr int kStage = TILE / 2;       // one 128-key tile of 8-bit rows: 16 KB
 constexpr int kBadBufs = 8;
 
-// Shared memory: Q0, Q1, then five K/V tiles; for 8-bit caches three tiles
-// and four staged 8-bit tiles.
+// Shared memory: Q0, Q1, four K/V tiles (for 8-bit caches three, and two
+// staged 8-bit tiles), and 4 KB for each softmax warp's results on their way
+// out.
 template <bool F8> struct Ring {
-    static constexpr int slots = F8 ? 3 : 5;
-    static constexpr int stages = F8 ? 4 : 0;
+    static constexpr int slots = F8 ? 3 : 4;
+    static constexpr int stages = F8 ? 2 : 0;
     static constexpr int threads = F8 ? 512 : 384;
     // launch registers and shares after the hand-over (setmaxnreg): the
     // shares add up to at most what the block was launched with
@@ -68,27 +74,31 @@ template <bool F8> struct Ring {
 };
 
 struct Work {
-    int b, q0, ql, kvl;        // sequence, its first packed row, its rows, its keys
-    int t0, nq;                // first token of this CTA (within the sequence), tokens
+    int q0, ql, kvl;           // the sequence's first packed row, its rows, its keys
+    int b, g, piece;           // sequence, KV head, piece
+    int t0;                    // first token of the item (within the sequence)
     int off;                   // position of token 0 of the sequence (kvl - ql; may be negative)
-    int j0, n, n0, n1;         // first key tile; tiles for the CTA, of row tile 0 and 1
-    int solo, go, partial;
+    int j0, n, n0, n1;         // first key tile; tiles of the item, of row tile 0 and 1
+    int solo, partial;
+    int go;                    // 0: no more items
 };
 
 struct RaggedBars {
-    uint64_t q_full;
+    uint64_t q_full, q_empty;             // q_empty: the MMAs have read Q (commit), and a warpgroup has no use for its place
     uint64_t kv_full[5], kv_empty[5];
     uint64_t st_full[4], st_empty[4];     // staged 8-bit tiles
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];
+    uint64_t work_full[2], work_empty[2];
     uint64_t vgo, vfix;                   // last value tile: there / its rows behind the end zeroed
+    uint64_t side_full;                   // solo: warpgroup 1's half is in shared memory
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    uint32_t bad_any[kBadBufs];           // key tile j has keys on pages outside the pool: bad[j % 8] says which
+    uint32_t bad_any[kBadBufs];           // K tile i of the CTA has keys on pages outside the pool: bad[i % 8] says which
     uint32_t bad[kBadBufs][4];
     uint8_t scale[2][128];                // 8-bit caches: scale bytes of the tile being widened
     float2 side[128];                     // solo: warpgroup 1's maximum and sum of each row
-    Work work;
+    Work work[2];
 };
 
 constexpr size_t kRaggedSmem = 1024 + 7 * TILE + sizeof(RaggedBars);
@@ -99,7 +109,7 @@ struct RaggedParams {
     int paged;
     int T, Hq, Hkv, G, tpt;    // tpt: tokens per 128-row tile (128 / G)
     int box_rows;              // keys one TMA box brings
-    int works, splits, chunk;  // launched work items; pieces per item; key tiles per piece
+    int works, splits, chunk;  // work items planned for; pieces per item; key tiles per piece
     float scale_log2;
     __nv_bfloat16 *out;
     float *lse;
@@ -129,7 +139,7 @@ __device__ __forceinline__ void seq_bounds(const RaggedParams &p, int b, int &q0
 // Which sequence and rows work item `idx` is (one warp).  Up to 32 sequences:
 // items in descending order of their keys, so that the longest start first.
 // More: in order, each sequence's last rows first.
-__device__ __forceinline__ bool find_work(const RaggedParams &p, int idx, Work *w) {
+__device__ __forceinline__ bool find_rows(const RaggedParams &p, int idx, Work *w) {
     const int lane = threadIdx.x & 31;
     const int qt = 2 * p.tpt;
     const int B = p.c.B;
@@ -193,12 +203,41 @@ __device__ __forceinline__ bool find_work(const RaggedParams &p, int idx, Work *
                       (p.paged && __ldg(p.c.kv_len + b) != w->kvl)))
         report(p.status, HS_ERR_INVALID_ARG);
     w->t0 = t * qt;
-    w->nq = min(qt, w->ql - w->t0);
     w->off = w->kvl - w->ql;
     return true;
 }
 
 __device__ __forceinline__ int key_tiles(int last_pos) { return last_pos < 0 ? 0 : last_pos / BN + 1; }
+
+// The i-th item of this CTA (one warp): items are numbered work, piece, KV
+// head (fastest) and dealt to the CTAs forth and back.
+__device__ __forceinline__ Work find_work(const RaggedParams &p, int i) {
+    Work w{};
+    const long long id = (long long)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (id >= (long long)p.works * p.splits * p.Hkv) return w;
+    const int item = (int)(id / p.Hkv);
+    w.g = (int)(id - (long long)item * p.Hkv);
+    w.piece = item % p.splits;
+    if (!find_rows(p, item / p.splits, &w)) return w;
+    const int nq = min(2 * p.tpt, w.ql - w.t0);
+    const int nk = key_tiles(w.off + w.t0 + nq - 1);
+    const int nk0 = key_tiles(w.off + w.t0 + min(p.tpt, nq) - 1);
+    w.solo = nq <= p.tpt;
+    w.j0 = min(w.piece * p.chunk, nk);
+    // (the last piece also takes keys past the length the plan was made for)
+    w.n = w.piece == p.splits - 1 ? nk - w.j0 : min(nk - w.j0, p.chunk);
+    if (w.solo) {
+        w.n0 = (w.n + 1) >> 1;
+        w.n1 = w.n >> 1;
+    } else {
+        w.n0 = min(max(nk0 - w.j0, 0), w.n);
+        w.n1 = w.n;
+    }
+    // one piece holds all the keys: no partial results for this item
+    w.partial = nk > p.chunk;
+    w.go = 1;
+    return w;
+}
 
 // Item `it` of the K/V sequence, in the order the MMAs consume it: with two
 // row tiles K0 V0 K1 V1 ...; solo, where two key tiles are in the air, K0 K1
@@ -231,12 +270,12 @@ struct RingPos {
     }
 };
 
-// Two 8-bit floats (low halves of both 16-bit lanes of `x`, i.e. x = code0 |
-// code1 << 16) to a bf16 pair scaled by 2^-120: the code's four exponent bits
-// go to the low end of the bf16 exponent, whose bias is larger by 120;
-// subnormal codes become subnormal bf16 numbers.
+// Two 8-bit floats (in the high bytes of both 16-bit halves of x) to a bf16
+// pair scaled by 2^-120: the sign stays, the code's four exponent bits go to
+// the low end of the bf16 exponent, whose bias is larger by 120; subnormal
+// codes become subnormal bf16 numbers.
 __device__ __forceinline__ uint32_t e4m3_to_bf16_tiny(uint32_t x) {
-    return ((x & 0x00800080u) << 8) | ((x & 0x007f007fu) << 4);
+    return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
 }
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -256,6 +295,86 @@ __device__ __forceinline__ bool all_128(bool yes) {
     return r != 0;
 }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+
+// Shared-memory descriptors (sdesc_sw128) in two words: the low one holds the
+// address / 16 and the leading byte offset / 16, the high one is the same for
+// every operand here (stride 1024 bytes, version 1, 128-byte swizzle).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescLboK = 16 >> 4;                    // K-major operands: not used by the 128-byte swizzle
+constexpr uint32_t kDescLboV = (HALF >> 4) - kDescLboK;    // what a value tile (N-major) has more: its halves lie 16 KB apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr >> 4) & 0x3fffu) | (kDescLboK << 16); }
+
+// mma_ss / mma_ts / mma_commit by the lane with leader != 0; every lane of
+// the warp calls them.
+__device__ __forceinline__ void mma_ss_one(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi,
+                                           uint32_t idesc, uint32_t accumulate, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+
+// A count of uses whose parity a barrier's waits follow.
+struct Phase {
+    uint32_t n = 0;
+    __device__ __forceinline__ uint32_t take() { return n++ & 1; }          // parity of the phase to wait for
+    __device__ __forceinline__ uint32_t take_free() { return (n++ & 1) ^ 1; }   // of the phase before it (free at the start)
+};
+
+// 2^x for two x in about [-126, 8]: 2^n by the exponent field, n = rint(x),
+// times a polynomial for the rest in [-0.5, 0.5] (degree 4, minimax in
+// relative error by the exchange algorithm: 2.6e-6, 1/1500 of a bf16
+// rounding, and 1.4e-8 on average, so sums of many keep fp32's accuracy).  It
+// runs on the FMA pipes beside the special-function unit, which at 16
+// results a clock would otherwise bound the softmax (128 x 128 x 2 per 2048
+// clocks of products).
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+    const float magic = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer, left in the low bits
+    x.x = fmaxf(x.x, -126.f);
+    x.y = fmaxf(x.y, -126.f);
+    const float2 t = fadd2(x, make_float2(magic, magic));
+    const float2 r = fadd2(t, make_float2(-magic, -magic));
+    const float2 f = ffma2(r, make_float2(-1.f, -1.f), x);
+    float2 y = ffma2(f, make_float2(0.00957010191f, 0.00957010191f), make_float2(0.0559178603f, 0.0559178603f));
+    y = ffma2(y, f, make_float2(0.240247448f, 0.240247448f));
+    y = ffma2(y, f, make_float2(0.693121815f, 0.693121815f));
+    y = ffma2(y, f, make_float2(0.999999261f, 0.999999261f));
+    return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
+
+// Of every 8 pairs of probabilities in a tile without masked keys, how many
+// come from exp2_fma.
+constexpr int kFmaPairs = 3;
+
 template <bool F8>
 __global__ void __launch_bounds__(Ring<F8>::threads, 1)
 ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -266,14 +385,14 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     uint8_t *sq = smem;
     uint8_t *skv = smem + 2 * TILE;
     uint8_t *sst = skv + R::slots * TILE;
+    uint8_t *so = smem + 6 * TILE;
     RaggedBars *bars = reinterpret_cast<RaggedBars *>(smem + 7 * TILE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = blockIdx.x % p.Hkv;
-    const int item = blockIdx.x / p.Hkv;
-    const int piece = item % p.splits;
+    constexpr int readers = F8 ? 15 : 11;      // warps that read each work item (all but the one that finds it)
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->q_full), 1);
+        mbar_init(smem_u32(&bars->q_empty), 1 + 128);
         for (int s = 0; s < 5; ++s) {
             mbar_init(smem_u32(&bars->kv_full[s]), F8 ? 128 : 1);
             mbar_init(smem_u32(&bars->kv_empty[s]), 1);
@@ -284,11 +403,16 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&bars->s_full[w]), 1);
-            mbar_init(smem_u32(&bars->p_full[w]), 128);
+            mbar_init(smem_u32(&bars->p_full[w][0]), 128);
+            mbar_init(smem_u32(&bars->p_full[w][1]), 128);
             mbar_init(smem_u32(&bars->o_full[w]), 1);
+            mbar_init(smem_u32(&bars->o_empty[w]), 128);
+            mbar_init(smem_u32(&bars->work_full[w]), 1);
+            mbar_init(smem_u32(&bars->work_empty[w]), readers);
         }
         mbar_init(smem_u32(&bars->vgo), 1);
         mbar_init(smem_u32(&bars->vfix), 32);
+        mbar_init(smem_u32(&bars->side_full), 128);
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_mbar_init();
@@ -297,296 +421,365 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
-    if (warp == 8) {
-        if (lane == 0) {
-            tma_prefetch(&tq);
-            tma_prefetch(&tk);
-            tma_prefetch(&tv);
-        }
-        Work w{};
-        const bool go = find_work(p, item / p.splits, &w);
-        if (go) {
-            const int nk = key_tiles(w.off + w.t0 + w.nq - 1);
-            const int nk0 = key_tiles(w.off + w.t0 + min(p.tpt, w.nq) - 1);
-            w.solo = w.nq <= p.tpt;
-            w.j0 = min(piece * p.chunk, nk);
-            // (the last piece also takes keys past the length the plan was made for)
-            w.n = piece == p.splits - 1 ? nk - w.j0 : min(nk - w.j0, p.chunk);
-            if (w.solo) {
-                w.n0 = (w.n + 1) >> 1;
-                w.n1 = w.n >> 1;
-            } else {
-                w.n0 = min(max(nk0 - w.j0, 0), w.n);
-                w.n1 = w.n;
-            }
-            // one piece holds all the keys: no partial results for this item
-            w.partial = nk > p.chunk;
-        }
-        w.go = go;
-        if (lane == 0) bars->work = w;
+    if (warp == 8 && lane == 0) {
+        tma_prefetch(&tq);
+        tma_prefetch(&tk);
+        tma_prefetch(&tv);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     volatile int *abort = &bars->abort;
-    const bool go = bars->work.go != 0;
-    const bool solo = bars->work.solo != 0;
-    const int n = bars->work.n;          // key tiles of this CTA (0: rows that see nothing, or an empty piece)
-    const int jb = bars->work.j0;
-    const int kvl = bars->work.kvl;
-    // value rows behind the sequence's end in the last tile
-    const int tail = go && n > 0 && (jb + n) * BN > kvl ? kvl - (jb + n - 1) * BN : BN;
+
+    // The next item, for a whole warp; false: none left, or a wait gave up
+    // (then *abort is set).
+    int work_i = 0;
+    Work wk;
+    auto next_work = [&]() -> bool {
+        const int slot = work_i & 1;
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->work_full[slot]), (work_i >> 1) & 1, p.wait_ns,
+                                                          abort));
+        if (!ok) return false;
+        wk = bars->work[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->work_empty[slot]));
+        ++work_i;
+        return wk.go != 0;
+    };
+    // value rows of the item's last tile that exist
+    auto tail_rows = [&]() { return (wk.j0 + wk.n) * BN > wk.kvl ? wk.kvl - (wk.j0 + wk.n - 1) * BN : BN; };
 
     if (warp >= 8) {
         regs_release<R::ctl>();
-        if (warp == 8 && go && n > 0) {
-            // ------------------------------------------------ TMA producer
-            const int q_row = bars->work.q0;
-            const int32_t *table = p.paged ? p.c.block_table + (size_t)bars->work.b * p.c.max_pages : nullptr;
-            const uint32_t qb = smem_u32(&bars->q_full);
-            if (lane == 0) {
-                const int tiles = solo ? 1 : 2;
-                mbar_expect_tx(qb, tiles * 2 * p.tpt * p.G * 128);
-                for (int s = 0; s < tiles; ++s)
-                    for (int hf = 0; hf < 2; ++hf)
-                        tma_load_3d(smem_u32(sq + s * TILE + hf * HALF), &tq, qb, hf * 64, g * p.G,
-                                    q_row + bars->work.t0 + s * p.tpt);
+        if (warp == 11) {
+            // ------------------------------------------------ items
+            for (int i = 0;; ++i) {
+                const Work w = find_work(p, i);
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->work_empty[i & 1]), ((i >> 1) & 1) ^ 1,
+                                                                  p.wait_ns, abort));
+                if (!ok) break;
+                if (lane == 0) {
+                    bars->work[i & 1] = w;
+                    mbar_arrive(smem_u32(&bars->work_full[i & 1]));
+                }
+                __syncwarp();
+                if (!w.go) break;
             }
+        } else if (warp == 8) {
+            // ------------------------------------------------ TMA producer
             constexpr int slots = F8 ? R::stages : R::slots;
             uint64_t *full = F8 ? bars->st_full : bars->kv_full;
             uint64_t *empty = F8 ? bars->st_empty : bars->kv_empty;
             constexpr int parts = F8 ? 1 : 2;        // boxes per group of rows (64-column halves of bf16 rows)
             constexpr int row_bytes = 128;           // per box row
             const int rshift = 31 - __clz(p.box_rows);
+            const uint32_t qb = smem_u32(&bars->q_full);
             RingPos pos;
-            int issued = 0;
+            Phase q_free;
+            uint32_t issued = 0, k_tiles = 0, q_loads = 0;
             bool ok = true;
-            for (int it = 0; it < 2 * n; ++it) {
-                int j;
-                bool is_v;
-                kv_item(it, n, solo, j, is_v);
-                const int key0 = (jb + j) * BN;
-                const int boxes = p.paged ? (min(BN, kvl - key0) + p.box_rows - 1) >> rshift : 1;
-                int page = 0;
-                if (p.paged && lane < boxes) page = __ldg(table + ((key0 + (lane << rshift)) >> p.c.page_shift));
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[pos.slot]), pos.phase ^ 1, p.wait_ns, abort));
+            while (ok && next_work()) {
+                const int n = wk.n;
+                if (n == 0) continue;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_empty), q_free.take_free(), p.wait_ns, abort));
                 if (!ok) break;
-                const uint32_t fb = smem_u32(&full[pos.slot]);
-                const uint32_t dst = smem_u32(F8 ? sst + pos.slot * kStage : skv + pos.slot * TILE);
-                const CUtensorMap *m = is_v ? &tv : &tk;
-                if (!is_v) {
-                    if (lane == 0) bars->bad_any[j % kBadBufs] = 0;
-                    if (lane < 4) bars->bad[j % kBadBufs][lane] = 0;
+                const bool solo = wk.solo != 0;
+                if (lane == 0) {
+                    const int tiles = solo ? 1 : 2;
+                    mbar_expect_tx(qb, tiles * 2 * p.tpt * p.G * 128);
+                    for (int s = 0; s < tiles; ++s)
+                        for (int hf = 0; hf < 2; ++hf)
+                            tma_load_3d(smem_u32(sq + s * TILE + hf * HALF), &tq, qb, hf * 64, wk.g * p.G,
+                                        wk.q0 + wk.t0 + s * p.tpt);
                 }
-                if (lane == 0) mbar_expect_tx(fb, (uint32_t)(boxes * p.box_rows * parts * row_bytes));
-                __syncwarp();
-                for (int i = lane; i < boxes; i += 32) {
-                    int c2 = 0, c3 = 0;
-                    if (p.paged) {
-                        const int key = key0 + (i << rshift);
-                        if (i >= 32) page = __ldg(table + (key >> p.c.page_shift));
-                        c2 = key & ((1 << p.c.page_shift) - 1);
-                        c3 = page;
-                        if (page < 0 || page >= p.c.num_pages) {
-                            // outside the pool: a box past the map's end reads zeros,
-                            // and the softmax leaves its keys out
-                            report(p.status, HS_ERR_INVALID_INDEX);
-                            c3 = p.c.num_pages;
-                            if (!is_v) {
-                                bars->bad_any[j % kBadBufs] = 1;
-                                for (int r = 0; r < p.box_rows; ++r)
-                                    atomicOr(&bars->bad[j % kBadBufs][((i << rshift) + r) >> 5],
-                                             1u << (((i << rshift) + r) & 31));
+                ++q_loads;
+                const int32_t *table = p.paged ? p.c.block_table + (size_t)wk.b * p.c.max_pages : nullptr;
+                for (int it = 0; it < 2 * n; ++it) {
+                    int j;
+                    bool is_v;
+                    kv_item(it, n, solo, j, is_v);
+                    const int key0 = (wk.j0 + j) * BN;
+                    const int boxes = p.paged ? (min(BN, wk.kvl - key0) + p.box_rows - 1) >> rshift : 1;
+                    int page = 0;
+                    if (p.paged && lane < boxes) page = __ldg(table + ((key0 + (lane << rshift)) >> p.c.page_shift));
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[pos.slot]), pos.phase ^ 1, p.wait_ns, abort));
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&full[pos.slot]);
+                    const uint32_t dst = smem_u32(F8 ? sst + pos.slot * kStage : skv + pos.slot * TILE);
+                    const CUtensorMap *m = is_v ? &tv : &tk;
+                    const int bad = (k_tiles + j) % kBadBufs;
+                    if (!is_v) {
+                        if (lane == 0) bars->bad_any[bad] = 0;
+                        if (lane < 4) bars->bad[bad][lane] = 0;
+                    }
+                    if (lane == 0) mbar_expect_tx(fb, (uint32_t)(boxes * p.box_rows * parts * row_bytes));
+                    __syncwarp();
+                    for (int i = lane; i < boxes; i += 32) {
+                        int c2 = wk.q0 + key0, c3 = 0;
+                        if (p.paged) {
+                            const int key = key0 + (i << rshift);
+                            if (i >= 32) page = __ldg(table + (key >> p.c.page_shift));
+                            c2 = key & ((1 << p.c.page_shift) - 1);
+                            c3 = page;
+                            if (page < 0 || page >= p.c.num_pages) {
+                                // outside the pool: a box past the map's end reads zeros,
+                                // and the softmax leaves its keys out
+                                report(p.status, HS_ERR_INVALID_INDEX);
+                                c3 = p.c.num_pages;
+                                if (!is_v) {
+                                    bars->bad_any[bad] = 1;
+                                    for (int r = i << rshift; r < (i + 1) << rshift; ++r)
+                                        atomicOr(&bars->bad[bad][r >> 5], 1u << (r & 31));
+                                }
                             }
                         }
-                    } else {
-                        c2 = q_row + key0;
+                        for (int hf = 0; hf < parts; ++hf)
+                            tma_load_4d(dst + hf * HALF + (i << rshift) * row_bytes, m, fb, hf * 64, wk.g, c2, c3);
                     }
-                    for (int hf = 0; hf < parts; ++hf)
-                        tma_load_4d(dst + hf * HALF + (i << rshift) * row_bytes, m, fb, hf * 64, g, c2, c3);
+                    ++issued;
+                    pos.next(slots);
                 }
-                issued = it + 1;
-                pos.next(slots);
+                k_tiles += n;
             }
             __syncwarp();
             if (lane == 0 && *abort) {   // let our own copies land before the CTA goes away
-                mbar_drain(qb, 0);
-                for (int it = issued > slots ? issued - slots : 0; it < issued; ++it)
+                if (q_loads > 0) mbar_drain(qb, (q_loads - 1) & 1);
+                for (uint32_t it = issued > (uint32_t)slots ? issued - slots : 0; it < issued; ++it)
                     mbar_drain(smem_u32(&full[it % slots]), (it / slots) & 1);
             }
-        } else if (warp == 9 && go && n > 0) {
+        } else if (warp == 9) {
             // ------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
-                const uint32_t qa[2] = {smem_u32(sq), smem_u32(sq + (solo ? 0 : TILE))};
-                const int nw[2] = {bars->work.n0, bars->work.n1};
-                int done_qk[2] = {0, 0}, done_pv[2] = {0, 0};
-                RingPos pos;
-                bool ok = mbar_wait(smem_u32(&bars->q_full), 0, p.wait_ns, abort);
-                auto kv_wait = [&]() {
-                    ok = ok && mbar_wait(smem_u32(&bars->kv_full[pos.slot]), pos.phase, p.wait_ns, abort);
-                    if (ok) tc_fence_after();
-                    return ok;
+            // The whole warp goes through the loop and one elected lane issues, so
+            // that descriptors stay in uniform registers: built in a single thread's
+            // branch they cost more than the products they start.
+            const uint32_t leader = elect_one();
+            const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+            const uint32_t q_lo[2] = {desc_lo(smem_u32(sq)), desc_lo(smem_u32(sq + TILE))};
+            const uint32_t kv_lo = desc_lo(smem_u32(skv));
+            Phase q_phase, o_free[2], p_phase[2], fix_phase;
+            RingPos pos;
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, abort));
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            while (ok && next_work()) {
+                const int n = __shfl_sync(0xffffffffu, wk.n, 0);
+                if (n == 0) continue;
+                const bool solo = __shfl_sync(0xffffffffu, wk.solo, 0) != 0;
+                const int n0 = __shfl_sync(0xffffffffu, wk.n0, 0), n1 = __shfl_sync(0xffffffffu, wk.n1, 0);
+                const bool fix = !F8 && __shfl_sync(0xffffffffu, tail_rows(), 0) < BN;
+                int done0 = 0, done1 = 0;
+                const uint32_t q1_lo = solo ? q_lo[0] : q_lo[1];
+                // S_w = Q_w K^T, K in the ring's current slot
+                auto qk = [&](auto w_) {
+                    constexpr int w = decltype(w_)::value;
+                    const uint32_t a = w == 0 ? q_lo[0] : q1_lo, b = kv_lo + pos.slot * (TILE >> 4);
+                    constexpr uint32_t I = idesc_bf16(128, 128, false, false);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t o = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                        mma_ss_one(tS[w], a + o, b + o, kDescHi, kDescHi, I, kk > 0 ? 1u : 0u, leader);
+                    }
+                    commit_one(smem_u32(&bars->s_full[w]), leader);
                 };
-                auto qk = [&](int w) {
-                    issue_qk(tS[w], qa[w], smem_u32(skv + pos.slot * TILE));
-                    mma_commit(smem_u32(&bars->s_full[w]));
-                    ++done_qk[w];
+                // O_w += P_w V, half by half as P arrives
+                auto pv = [&](auto w_, int slot, int &done, int all) {
+                    constexpr int w = decltype(w_)::value;
+                    constexpr uint32_t I = idesc_bf16(128, 128, false, true);
+                    const uint32_t parity = p_phase[w].take();
+                    const uint32_t b = kv_lo + slot * (TILE >> 4);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!wait(&bars->p_full[w][half], parity)) return;
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            mma_ts_one(tO[w], tS[w] + kk * 8, b + ((kk * 2048) >> 4) + (kDescLboV << 16), kDescHi, I,
+                                       (kk > 0 || done > 0) ? 1u : 0u, leader);
+                    }
+                    if (++done == all) commit_one(smem_u32(&bars->o_full[w]), leader);
                 };
-                auto pv = [&](int w, uint32_t v_addr) {
-                    ok = mbar_wait(smem_u32(&bars->p_full[w]), done_pv[w] & 1, p.wait_ns, abort);
-                    if (!ok) return;
-                    tc_fence_after();
-                    issue_pv(tO[w], tS[w], v_addr, done_pv[w] > 0);
-                    if (++done_pv[w] == nw[w]) mma_commit(smem_u32(&bars->o_full[w]));
-                };
+                constexpr std::integral_constant<int, 0> W0{};
+                constexpr std::integral_constant<int, 1> W1{};
                 // the last value tile may have rows to be zeroed first
                 auto tail_wait = [&](int j) {
-                    if (!F8 && j == n - 1 && tail < BN) {
-                        mbar_arrive(smem_u32(&bars->vgo));
-                        ok = ok && mbar_wait(smem_u32(&bars->vfix), 0, p.wait_ns, abort);
-                        if (ok) tc_fence_after();
+                    if (fix && j == n - 1) {
+                        if (leader) mbar_arrive(smem_u32(&bars->vgo));
+                        wait(&bars->vfix, fix_phase.take());
                     }
+                    return ok;
                 };
-                auto release = [&]() {
-                    mma_commit(smem_u32(&bars->kv_empty[pos.slot]));
-                    pos.next(R::slots);
-                };
+                auto release = [&](int slot) { commit_one(smem_u32(&bars->kv_empty[slot]), leader); };
+                auto kv_wait = [&]() { return wait(&bars->kv_full[pos.slot], pos.phase); };
+                if (!wait(&bars->q_full, q_phase.take()) || !kv_wait()) break;
                 if (!solo) {
-                    if (kv_wait()) {
-                        for (int w = 0; w < 2; ++w)
-                            if (nw[w] > 0) qk(w);
-                        release();
-                    }
-                    for (int j = 0; ok && j < n; ++j) {
+                    if (n0 > 0) qk(W0);
+                    qk(W1);
+                    release(pos.slot);
+                    pos.next(R::slots);
+                    if (n == 1) commit_one(smem_u32(&bars->q_empty), leader);
+                } else {
+                    qk(W0);
+                    release(pos.slot);
+                    pos.next(R::slots);
+                    if (n > 1) {
                         if (!kv_wait()) break;
-                        tail_wait(j);
-                        if (!ok) break;
-                        const RingPos vpos = pos;
-                        const uint32_t v_addr = smem_u32(skv + vpos.slot * TILE);
+                        qk(W1);
+                        release(pos.slot);
                         pos.next(R::slots);
-                        bool have_k = false;
-                        for (int w = 0; ok && w < 2; ++w) {
-                            if (j < nw[w]) pv(w, v_addr);
-                            if (ok && w == 1) mma_commit(smem_u32(&bars->kv_empty[vpos.slot]));
-                            if (ok && j + 1 < nw[w]) {
-                                if (!have_k && !kv_wait()) break;
-                                have_k = true;
-                                qk(w);
+                    }
+                    if (n <= 2) commit_one(smem_u32(&bars->q_empty), leader);
+                }
+                // O may be overwritten once the item that had it before has been read out
+                if (n0 > 0 && !wait(&bars->o_empty[0], o_free[0].take_free())) break;
+                if (n1 > 0 && !wait(&bars->o_empty[1], o_free[1].take_free())) break;
+                if (!solo) {
+                    for (int j = 0; j < n; ++j) {          // n1 = n >= n0
+                        if (!kv_wait() || !tail_wait(j)) break;
+                        const int v_slot = pos.slot;
+                        pos.next(R::slots);
+                        const bool more = j + 1 < n;
+                        if (j < n0) {
+                            pv(W0, v_slot, done0, n0);
+                            if (!ok) break;
+                            if (j + 1 < n0) {
+                                if (!kv_wait()) break;
+                                qk(W0);
                             }
                         }
-                        if (ok && have_k) release();
+                        pv(W1, v_slot, done1, n1);
+                        if (!ok) break;
+                        release(v_slot);
+                        if (more) {
+                            if (!kv_wait()) break;
+                            qk(W1);
+                            release(pos.slot);
+                            pos.next(R::slots);
+                            if (j + 2 == n) commit_one(smem_u32(&bars->q_empty), leader);   // the last product with Q
+                        }
                     }
                 } else {
-                    for (int j = 0; ok && j < min(n, 2); ++j) {
-                        if (!kv_wait()) break;
-                        qk(j);
-                        release();
-                    }
-                    for (int j = 0; ok && j < n; ++j) {
-                        if (!kv_wait()) break;
-                        tail_wait(j);
+                    for (int j = 0; j < n; ++j) {
+                        if (!kv_wait() || !tail_wait(j)) break;
+                        if (j & 1) pv(W1, pos.slot, done1, n1);
+                        else pv(W0, pos.slot, done0, n0);
                         if (!ok) break;
-                        pv(j & 1, smem_u32(skv + pos.slot * TILE));
-                        if (!ok) break;
-                        release();
+                        release(pos.slot);
+                        pos.next(R::slots);
                         if (j + 2 < n) {
                             if (!kv_wait()) break;
-                            qk(j & 1);
-                            release();
+                            if (j & 1) qk(W1);
+                            else qk(W0);
+                            release(pos.slot);
+                            pos.next(R::slots);
+                            if (j + 3 == n) commit_one(smem_u32(&bars->q_empty), leader);
                         }
                     }
                 }
-                // all MMAs this thread issued have completed before TMEM is freed
-                mma_commit(smem_u32(&bars->drain));
-                mbar_drain(smem_u32(&bars->drain), 0);
             }
-        } else if (!F8 && warp == 10 && go && tail < BN) {
+            // all MMAs this warp issued have completed before TMEM is freed
+            commit_one(smem_u32(&bars->drain), leader);
+            if (leader) mbar_drain(smem_u32(&bars->drain), 0);
+            __syncwarp();
+        } else if (warp == 10) {
             // ------------------------------------------------ value rows behind the end
-            // (the MMA thread, which has waited for the tile, says when)
-            const int slot = (2 * n - 1) % R::slots;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->vgo), 0, p.wait_ns, abort));
-            if (ok) {
-                // whole 128-byte rows, so the swizzle within a row does not matter
-                for (int i = lane; i < (BN - tail) * 16; i += 32) {
-                    const int row = tail + (i >> 4), part = i & 15;
-                    *reinterpret_cast<uint4 *>(skv + slot * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
+            Phase go;
+            uint32_t items = 0;     // K and V tiles before this item
+            while (next_work()) {
+                const int tail = tail_rows();
+                if (!F8 && wk.n > 0 && tail < BN) {
+                    // (the MMA thread, which has waited for the tile, says when)
+                    const int slot = (items + 2 * wk.n - 1) % R::slots;
+                    const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->vgo), go.take(), p.wait_ns, abort));
+                    if (!ok) break;
+                    // whole 128-byte rows, so the swizzle within a row does not matter
+                    for (int i = lane; i < (BN - tail) * 16; i += 32) {
+                        const int row = tail + (i >> 4), part = i & 15;
+                        *reinterpret_cast<uint4 *>(skv + slot * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&bars->vfix));
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&bars->vfix));
+                items += 2 * wk.n;
             }
-        } else if (F8 && warp >= 12 && go && n > 0) {
+        } else if (F8) {
             // ------------------------------------------------ 8-bit rows to bf16 tiles
             const int t = threadIdx.x - 384;
-            const int32_t *table = p.c.block_table + (size_t)bars->work.b * p.c.max_pages;
             const int c16 = t & 7, r0 = t >> 3;      // 16 codes of rows r0, r0 + 16, ...
-            auto scale_load = [&](int it) -> int {   // scale byte of this thread's row (t) of item `it`
-                if (it >= 2 * n) return 0;
-                int j;
-                bool is_v;
-                kv_item(it, n, solo, j, is_v);
-                const int key = (jb + j) * BN + t;
-                if (key >= kvl) return 0;
-                const int page = __ldg(table + (key >> p.c.page_shift));
-                if (page < 0 || page >= p.c.num_pages) return 0;
-                const uint8_t *s = is_v ? p.c.v_scale : p.c.k_scale;
-                return __ldg(s + (((size_t)page * p.Hkv + g) << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1)));
-            };
+            // the two 16-byte chunks these codes become, of the row's 16 (8 a half);
+            // lanes of the second half store them in the other order, so that the
+            // eight lanes of a store phase touch all banks
+            const bool second = c16 >= 4;
+            const int ch0 = ((2 * c16) & 7) + (second ? 1 : 0), ch1 = ((2 * c16) & 7) + (second ? 0 : 1);
+            const uint32_t row_at = (c16 >> 2) * HALF + r0 * 128;
+            const uint32_t at0 = row_at + ((ch0 ^ (r0 & 7)) << 4), at1 = row_at + ((ch1 ^ (r0 & 7)) << 4);
             RingPos st, kv;
-            int byte = scale_load(0);
+            uint32_t tiles = 0;
             bool ok = true;
-            for (int it = 0; it < 2 * n; ++it) {
-                bars->scale[it & 1][t] = (uint8_t)byte;
-                byte = scale_load(it + 1);
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->st_full[st.slot]), st.phase, p.wait_ns, abort));
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_empty[kv.slot]), kv.phase ^ 1, p.wait_ns,
-                                                             abort));
-                // the four warps meet here for the scale bytes, and leave together when
-                // one of them gave up waiting
-                if (!all_128(ok)) break;
-                const uint8_t *src = sst + st.slot * kStage;
-                uint8_t *dst = skv + kv.slot * TILE;
-                const int live = it == 2 * n - 1 ? tail : BN;   // value rows behind the end are zeroed
+            while (all_128(ok && next_work())) {     // the four warps go on, or leave, together
+                const int n = wk.n;
+                const bool solo = wk.solo != 0;
+                const int32_t *table = p.c.block_table + (size_t)wk.b * p.c.max_pages;
+                // scale byte of this thread's row (t) of item `it`; 0: no such row (it becomes zeros)
+                auto scale_load = [&](int it) -> int {
+                    if (it >= 2 * n) return 0;
+                    int j;
+                    bool is_v;
+                    kv_item(it, n, solo, j, is_v);
+                    const int key = (wk.j0 + j) * BN + t;
+                    if (key >= wk.kvl) return 0;
+                    const int page = __ldg(table + (key >> p.c.page_shift));
+                    if (page < 0 || page >= p.c.num_pages) return 0;
+                    const uint8_t *s = is_v ? p.c.v_scale : p.c.k_scale;
+                    return __ldg(s + (((size_t)page * p.Hkv + wk.g) << p.c.page_shift) +
+                                 (key & ((1 << p.c.page_shift) - 1)));
+                };
+                int byte = scale_load(0);
+                for (int it = 0; it < 2 * n; ++it, ++tiles) {
+                    const int buf = tiles & 1;
+                    bars->scale[buf][t] = (uint8_t)byte;
+                    byte = scale_load(it + 1);
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->st_full[st.slot]), st.phase, p.wait_ns, abort));
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_empty[kv.slot]), kv.phase ^ 1,
+                                                                 p.wait_ns, abort));
+                    // the four warps meet here for the scale bytes, and leave together when
+                    // one of them gave up waiting
+                    ok = all_128(ok);
+                    if (!ok) break;
+                    const uint8_t *src = sst + st.slot * kStage + r0 * 128 + c16 * 16;
+                    uint8_t *dst = skv + kv.slot * TILE;
+                    // rows that are not there keep finite leftovers: their probabilities are exactly 0
 #pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                    const int row = r0 + 16 * i;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(src + row * 128 + c16 * 16);
-                    const int e = (int)bars->scale[it & 1][row] - 7;          // 120 + (byte - 127)
-                    const int e1 = max(min(e, 127), -126), e2 = min(e - e1, 127);
-                    const uint32_t f1 = (uint32_t)(e1 + 127) * 0x00800080u;
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t o[8];
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(src + i * 2048);
+                        const uint32_t sb = bars->scale[buf][r0 + 16 * i];
+                        // 2^(120 + byte - 127) as a bf16 pair, up to 2^127
+                        uint32_t f = min(sb, 134u) * 0x00800080u + 0x3c003c00u;
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t o[8];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny(__byte_perm(w[q], 0, 0x4140)), f1);
-                        o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny(__byte_perm(w[q], 0, 0x4342)), f1);
-                    }
-                    if (e2 != 0) {       // scales above 2^7 take a second power of two
-                        const uint32_t f2 = (uint32_t)(e2 + 127) * 0x00800080u;
+                        for (int q = 0; q < 4; ++q) {
+                            o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny(__byte_perm(w[q], 0, 0x1404)), f);
+                            o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny(__byte_perm(w[q], 0, 0x3424)), f);
+                        }
+                        if (sb > 134u) {       // the rest of a scale above 2^7
+                            f = (sb - 134u) * 0x00800080u + 0x3f803f80u;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = bf16x2_mul(o[q], f2);
+                            for (int q = 0; q < 8; ++q) o[q] = bf16x2_mul(o[q], f);
+                        }
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4 *>(dst + at0 + i * 2048) = second ? hi : lo;
+                        *reinterpret_cast<uint4 *>(dst + at1 + i * 2048) = second ? lo : hi;
                     }
-                    if (row >= live) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = 0;
-                    }
-                    // chunks 2 c16 and 2 c16 + 1 of the row's 16 (8 a half); lanes of
-                    // the second half store them in the other order, so that the
-                    // eight lanes of a store phase touch all banks
-                    uint8_t *row_dst = dst + (c16 >> 2) * HALF + row * 128;
-                    const int c0 = (2 * c16) & 7;
-                    const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-                    const bool second = c16 >= 4;
-                    *reinterpret_cast<uint4 *>(row_dst + (((c0 + (second ? 1 : 0)) ^ (row & 7)) << 4)) = second ? b : a;
-                    *reinterpret_cast<uint4 *>(row_dst + (((c0 + (second ? 0 : 1)) ^ (row & 7)) << 4)) = second ? a : b;
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&bars->kv_full[kv.slot]));
+                    mbar_arrive(smem_u32(&bars->st_empty[st.slot]));
+                    st.next(R::stages);
+                    kv.next(R::slots);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&bars->kv_full[kv.slot]));
-                mbar_arrive(smem_u32(&bars->st_empty[st.slot]));
-                st.next(R::stages);
-                kv.next(R::slots);
             }
         }
     } else {
@@ -594,186 +787,265 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         // ------------------------------------------------ softmax warpgroups
         const int w = warp >> 2;
         const int tw = threadIdx.x - 128 * w;
-        const int tok = bars->work.t0 + (solo ? 0 : w * p.tpt) + tw / p.G;
-        const int h = g * p.G + tw % p.G;
-        const bool valid = go && tw < p.tpt * p.G && tok < bars->work.ql;
-        const int pos = bars->work.off + min(tok, bars->work.ql - 1);
-        // a key tile with any key past this position needs the causal mask
-        const int pos_first = bars->work.off + bars->work.t0 + (solo ? 0 : w * p.tpt);
         const uint32_t lane_off = (uint32_t)(tw & ~31) << 16;
         const uint32_t tS = tmem + lane_off + (uint32_t)(w * 128);
         const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(w * 128);
         const float c2 = p.scale_log2;
-        const int nw = go ? (w == 0 ? bars->work.n0 : bars->work.n1) : 0;
-        float m = -INFINITY, l = 0.f;
+        const float nan = __int_as_float(0x7fc00000);
+        const int row_tok = tw / p.G, row_head = tw - row_tok * p.G;
+        Phase s_phase, o_phase, side_phase;
+        uint32_t k_tiles = 0;
         bool ok = true;
-        for (int i = 0; i < nw; ++i) {
-            const int j = solo ? 2 * i + w : i;
-            const int key0 = (jb + j) * BN;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[w]), i & 1, p.wait_ns, abort));
-            if (!ok) break;
-            tc_fence_after();
-            // S_i is there, and P V of the previous tile (issued before it) is done
-            float s[128];
-            {
-                uint32_t r[4][32];
+        while (ok && next_work()) {
+            const bool solo = wk.solo != 0;
+            const int n = wk.n;
+            const int first = wk.t0 + (solo ? 0 : w * p.tpt);      // this row tile's first token
+            const int tok = first + row_tok;
+            const bool valid = tw < p.tpt * p.G && tok < wk.ql;
+            const int pos = wk.off + min(tok, wk.ql - 1);
+            const int pos_first = wk.off + first;
+            const int nw = w == 0 ? wk.n0 : wk.n1;
+            const bool join = solo && n > 1;
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < nw; ++i) {
+                const int j = solo ? 2 * i + w : i;
+                const int key0 = (wk.j0 + j) * BN;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[w]), s_phase.take(), p.wait_ns, abort));
+                if (!ok) break;
+                tc_fence_after();
+                // Q's place is only needed here again when the halves are joined there
+                // (then warpgroup 0 says when it is done with it)
+                if (i == 0 && !join && w == (solo ? 0 : 1)) mbar_arrive(smem_u32(&bars->q_empty));
+                // S_i is there, and P V of the previous tile (issued before it) is done
+                float s[128];
+                {
+                    uint32_t r[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
-                tmem_wait_ld();
+                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(r[c >> 5][c & 31]);
-            }
-            if (key0 + BN - 1 > pos_first) {
+                    for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(r[c >> 5][c & 31]);
+                }
+                const int bad = (k_tiles + j) % kBadBufs;
+                const bool lost = p.paged && bars->bad_any[bad] != 0;
+                const bool masked = lost || key0 + BN - 1 > pos_first;
+                if (masked) {
+                    // one bit a key: up to the row's own position, and not on a lost page
+                    const int seen = pos - key0 + 1;
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (key0 + c > pos) s[c] = -INFINITY;
-            }
-            if (p.paged && bars->bad_any[j % kBadBufs]) {
+                    for (int q = 0; q < 4; ++q) {
+                        const int k = min(max(seen - 32 * q, 0), 32);
+                        uint32_t bits = k == 32 ? 0xffffffffu : (1u << k) - 1u;
+                        if (lost) bits &= ~bars->bad[bad][q];
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if ((bars->bad[j % kBadBufs][c >> 5] >> (c & 31)) & 1u) s[c] = -INFINITY;
-            }
-            float m4[4] = {s[0], s[1], s[2], s[3]};
+                        for (int c = 0; c < 32; ++c)
+                            if (!((bits >> c) & 1u)) s[32 * q + c] = -INFINITY;
+                    }
+                }
+                float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < 128; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
-            const float mx2 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
-            // the running maximum only moves when it grows by more than 8 (log2
-            // units); the final division uses the same reference
-            if (__any_sync(0xffffffffu, mx2 > m + 8.0f)) {
-                const float m_new = fmaxf(m, mx2);
-                if (i > 0) {
-                    const float corr = m_new == -INFINITY ? 1.f : ex2(m - m_new);
-                    l *= corr;
+                for (int c = 4; c < 128; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+                const float mx2 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+                // the running maximum only moves when it grows by more than 8 (log2
+                // units); the final division uses the same reference
+                if (__any_sync(0xffffffffu, mx2 > m + 8.0f)) {
+                    const float m_new = fmaxf(m, mx2);
+                    if (i > 0) {
+                        const float corr = m_new == -INFINITY ? 1.f : ex2(m - m_new);
+                        l *= corr;
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + 16 * c, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                        tmem_st16(tO + 16 * c, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                            tmem_st16(tO + 16 * c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    m = m_new;
+                }
+                const float mref = m == -INFINITY ? 0.f : m;   // masked keys (-inf) give 2^-inf = 0
+                const float2 c2v = make_float2(c2, c2), mv = make_float2(-mref, -mref);
+                float2 ps01 = make_float2(0.f, 0.f), ps23 = make_float2(0.f, 0.f);
+                // 64 keys to P: every 16 columns of bf16 pairs leave as soon as they are done
+                auto probabilities = [&](int half, auto fma_pairs) {
+#pragma unroll
+                    for (int ch = 2 * half; ch < 2 * half + 2; ++ch) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int c = ch * 32 + 2 * e;
+                            const float2 t = ffma2(make_float2(s[c], s[c + 1]), c2v, mv);
+                            const float2 ab = (e & 7) < decltype(fma_pairs)::value ? exp2_fma(t)
+                                                                                   : make_float2(ex2(t.x), ex2(t.y));
+                            if (e & 1) ps23 = fadd2(ps23, ab); else ps01 = fadd2(ps01, ab);
+                            // P is rounded to bf16, the type of V: one MMA takes one type
+                            pk[e] = pack_bf16(ab.x, ab.y);
+                        }
+                        tmem_st16(tS + 16 * ch, pk);
                     }
                     tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&bars->p_full[w][half]));
+                };
+                if (masked) {          // exp2_fma would not give 0 for a masked key
+                    probabilities(0, std::integral_constant<int, 0>());
+                    probabilities(1, std::integral_constant<int, 0>());
+                } else {
+                    probabilities(0, std::integral_constant<int, kFmaPairs>());
+                    probabilities(1, std::integral_constant<int, kFmaPairs>());
                 }
-                m = m_new;
+                l += (ps01.x + ps01.y) + (ps23.x + ps23.y);
             }
-            const float mref = m == -INFINITY ? 0.f : m;   // masked keys (-inf) give 2^-inf = 0
-            const float2 c2v = make_float2(c2, c2), mv = make_float2(-mref, -mref);
-            float2 ps01 = make_float2(0.f, 0.f), ps23 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {            // 32 keys, 16 TMEM columns of bf16 pairs
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int c = ch * 32 + 2 * e;
-                    const float2 t = ffma2(make_float2(s[c], s[c + 1]), c2v, mv);
-                    const float2 ab = make_float2(ex2(t.x), ex2(t.y));
-                    if (e & 1) ps23 = fadd2(ps23, ab); else ps01 = fadd2(ps01, ab);
-                    // P is rounded to bf16, the type of V: one MMA takes one type
-                    pk[e] = pack_bf16(ab.x, ab.y);
+            k_tiles += n;
+            if (nw > 0)
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&bars->o_full[w]), o_phase.take(), p.wait_ns, abort));
+            bool fin = ok;
+            tc_fence_after();
+            // O of this thread's row: columns [16 c, 16 c + 16), zeros when there were no tiles
+            auto load_o = [&](int c, float (&o)[16]) {
+                uint32_t r[16];
+                if (nw > 0) {
+                    tmem_ld16(tO + 16 * c, r);
+                    tmem_wait_ld();
                 }
-                tmem_st16(tS + 16 * ch, pk);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = nw > 0 ? __uint_as_float(r[e]) : 0.f;
+            };
+            float *const side = reinterpret_cast<float *>(sq) + tw * 128;   // 64 KB: the Q tiles, no longer read
+            float a0 = 1.f, a1 = 0.f;
+            if (join) {
+                // warpgroup 1 hands its half of the keys over through shared memory
+                if (w == 1) {
+                    bars->side[tw] = make_float2(fin ? m : nan, l);
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        load_o(c, o);
+                        if (valid) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<float4 *>(side + (((4 * c + e) ^ (tw & 31)) << 2)) =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                    fence_proxy_async_smem();      // the next Q tiles come here through the async proxy
+                    mbar_arrive(smem_u32(&bars->side_full));
+                } else {
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->side_full), side_phase.take(), p.wait_ns, abort));
+                    if (!ok) fin = false;
+                    const float2 other = bars->side[tw];
+                    const float top = fmaxf(m, other.x);
+                    if (other.x != other.x) fin = false;
+                    a0 = m == -INFINITY ? 0.f : ex2(m - top);
+                    a1 = other.x == -INFINITY ? 0.f : ex2(other.x - top);
+                    l = l * a0 + other.y * a1;
+                    m = top;
+                }
             }
-            l += (ps01.x + ps01.y) + (ps23.x + ps23.y);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(smem_u32(&bars->p_full[w]));
-        }
-        bool fin = ok;
-        if (nw > 0)
-            fin = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&bars->o_full[w]), 0, p.wait_ns, abort));
-        tc_fence_after();
-        // O of this thread's row: columns [16 c, 16 c + 16), zeros when there were no tiles
-        auto load_o = [&](int c, float (&o)[16]) {
-            uint32_t r[16];
+            const bool partial = wk.partial != 0;
+            const size_t row = (size_t)wk.q0 + tok;
+            const int h = wk.g * p.G + row_head;
+            // the row's result is this item's to write: not warpgroup 1's of a shared
+            // tile, and not an empty piece's of a row that one piece holds
+            const bool mine = !(solo && w == 1);
+            if (valid && mine && (partial || wk.piece == 0)) {
+                const size_t pr = ((size_t)wk.piece * p.T + row) * p.Hq + h;
+                if (partial) p.part_ml[pr] = make_float2(fin ? m : nan, l);
+                else {
+                    if (p.splits > 1) p.part_ml[pr] = make_float2(0.f, -1.f);
+                    // a bounded wait gave up: NaN in the row's lse, as in the full layer
+                    p.lse[(size_t)h * p.T + row] = !fin ? nan : (l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY);
+                }
+            }
+            if (mine && (partial ? n > 0 : wk.piece == 0)) {
+                const float inv_l = partial ? 1.f : (l > 0.f ? 1.0f / l : 0.f);   // a row that sees nothing gives zeros
+                a0 *= inv_l;
+                a1 *= inv_l;
+                // Through shared memory, 32 rows x 128 bytes of a warp at a time, so that
+                // a store writes whole 128-byte lines (a thread's own row would be 32 of
+                // them a store).  Chunk c of row r lies at c ^ (r & 7).
+                uint8_t *stage = so + (warp & 7) * 4096;
+                uint8_t *mine_at = stage + lane * 128;
+                const int rows32 = tw & ~31;
+                const int steps = partial ? 4 : 2;
+#pragma unroll 1
+                for (int c = 0; c < steps; ++c) {
+                    __syncwarp();                              // the step before has been read
+#pragma unroll 1
+                    for (int q = 0; q < (partial ? 2 : 4); ++q) {       // 16 columns each
+                        float o[16];
+                        const int col = partial ? 2 * c + q : 4 * c + q;
+                        load_o(col, o);
+                        if (join) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 y = *reinterpret_cast<const float4 *>(side + (((4 * col + e) ^ (tw & 31)) << 2));
+                                o[4 * e] = o[4 * e] * a0 + y.x * a1;
+                                o[4 * e + 1] = o[4 * e + 1] * a0 + y.y * a1;
+                                o[4 * e + 2] = o[4 * e + 2] * a0 + y.z * a1;
+                                o[4 * e + 3] = o[4 * e + 3] * a0 + y.w * a1;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= a0;
+                        }
+                        if (partial) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<float4 *>(mine_at + (((4 * q + e) ^ (lane & 7)) << 4)) =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<uint4 *>(mine_at + (((2 * q + e) ^ (lane & 7)) << 4)) =
+                                    make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                               pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int r0 = 0; r0 < 32; r0 += 4) {       // four rows a store, eight lanes each
+                        const int r = r0 + (lane >> 3), ch = lane & 7;
+                        const int tr = rows32 + r, t_tok = tr / p.G, t = first + t_tok;
+                        if (tr < p.tpt * p.G && t < wk.ql) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+                            const size_t at = (size_t)(wk.q0 + t) * p.Hq + wk.g * p.G + (tr - t_tok * p.G);
+                            if (partial)
+                                *reinterpret_cast<uint4 *>(p.part_o + ((size_t)wk.piece * p.T * p.Hq + at) * HD + 32 * c + 4 * ch) = x;
+                            else
+                                *reinterpret_cast<uint4 *>(p.out + at * HD + 64 * c + 8 * ch) = x;
+                        }
+                    }
+                }
+            }
+            if (w == 0 && join) {
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&bars->q_empty));
+            }
             if (nw > 0) {
-                tmem_ld16(tO + 16 * c, r);
-                tmem_wait_ld();
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = nw > 0 ? __uint_as_float(r[e]) : 0.f;
-        };
-        const bool join = go && solo && n > 1;
-        float *const side = reinterpret_cast<float *>(sq) + tw * 128;   // 64 KB: the Q tiles, no longer read
-        float a0 = 1.f, a1 = 0.f;
-        if (join) {
-            // warpgroup 1 hands its half of the keys over through shared memory
-            if (w == 1) {
-                bars->side[tw] = make_float2(fin ? m : __int_as_float(0x7fc00000), l);
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    float o[16];
-                    load_o(c, o);
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<float4 *>(side + (((4 * c + e) ^ (tw & 31)) << 2)) =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    }
-                }
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (w == 0) {
-                const float2 other = bars->side[tw];
-                const float top = fmaxf(m, other.x);
-                if (other.x != other.x) fin = false;
-                a0 = m == -INFINITY ? 0.f : ex2(m - top);
-                a1 = other.x == -INFINITY ? 0.f : ex2(other.x - top);
-                l = l * a0 + other.y * a1;
-                m = top;
+                tc_fence_before();
+                mbar_arrive(smem_u32(&bars->o_empty[w]));
             }
         }
-        const bool partial = bars->work.partial != 0;
-        // the row's result is this CTA's to write: not warpgroup 1 of a shared
-        // tile, and not an empty piece of an item that one piece holds
-        if (valid && !(solo && w == 1) && (partial || piece == 0)) {
-            const size_t row = (size_t)bars->work.q0 + tok;
-            const size_t pr = ((size_t)piece * p.T + row) * p.Hq + h;
-            const float bad = __int_as_float(0x7fc00000);
-            if (partial) p.part_ml[pr] = make_float2(fin ? m : bad, l);
-            else {
-                if (p.splits > 1) p.part_ml[pr] = make_float2(0.f, -1.f);
-                // a bounded wait gave up: NaN in the row's lse, as in the full layer
-                p.lse[(size_t)h * p.T + row] = !fin ? bad : (l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY);
-            }
-        }
-        if (go && !(solo && w == 1) && (partial ? n > 0 : piece == 0)) {
-            const size_t row = (size_t)bars->work.q0 + tok;
-            const float inv_l = partial ? 1.f : (l > 0.f ? 1.0f / l : 0.f);   // a row that sees nothing gives zeros
-            a0 *= inv_l;
-            a1 *= inv_l;
-            __nv_bfloat16 *orow = p.out + (row * p.Hq + h) * HD;
-            float *prow = p.part_o + (((size_t)piece * p.T + row) * p.Hq + h) * HD;
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-                float o[16];
-                load_o(c, o);
-                if (!valid) continue;
-                if (join) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 y = *reinterpret_cast<const float4 *>(side + (((4 * c + e) ^ (tw & 31)) << 2));
-                        o[4 * e] = o[4 * e] * a0 + y.x * a1;
-                        o[4 * e + 1] = o[4 * e + 1] * a0 + y.y * a1;
-                        o[4 * e + 2] = o[4 * e + 2] * a0 + y.z * a1;
-                        o[4 * e + 3] = o[4 * e + 3] * a0 + y.w * a1;
+        // a wait gave up: the rows of the items that this CTA did not get to
+        // are marked like those of the one it was at
+        if (*abort && (warp & 3) == 0) {
+            for (int i = work_i;; ++i) {
+                const Work x = find_work(p, i);
+                if (!x.go) break;
+                if (x.solo && w == 1) continue;
+                for (int r = lane; r < p.tpt * p.G; r += 32) {
+                    const int tok = x.t0 + (x.solo ? 0 : w * p.tpt) + r / p.G, h = x.g * p.G + r % p.G;
+                    if (tok >= x.ql) continue;
+                    const size_t row = (size_t)x.q0 + tok;
+                    if (x.partial) p.part_ml[((size_t)x.piece * p.T + row) * p.Hq + h] = make_float2(nan, 1.f);
+                    else if (x.piece == 0) {
+                        if (p.splits > 1) p.part_ml[row * p.Hq + h] = make_float2(0.f, -1.f);
+                        p.lse[(size_t)h * p.T + row] = nan;
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] *= a0;
-                }
-                if (partial) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<float4 *>(prow + 16 * c + 4 * e) =
-                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
-                    uint32_t pk[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(o[2 * e], o[2 * e + 1]);
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + 16 * c);
-                    dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
             }
         }
@@ -876,6 +1148,19 @@ constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an
 constexpr int kFewRowsFixed = 8;           // what a piece costs besides its keys, in 16-key blocks
 constexpr int kFewRowsMinChunk = 4;        // fewest 16-key blocks in a piece (one for each warp)
 constexpr size_t kMaxPartRows = 180000;    // rows of partial results: 520 bytes each
+
+// SMs of the current device (one CTA of the tcgen05 kernel runs on each).
+int sm_count() {
+    static std::atomic<int> cached[64]{};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kSms;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kSms;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 // Work items of a batch (an upper bound from what the host knows).
 long long work_bound(const RaggedCall &a) {
@@ -1002,12 +1287,13 @@ cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *
                !map_keys(&mv, a.v, a.Hkv, a.T, a.ld_v, 1, p.box_rows, false)) {
         return cudaErrorInvalidValue;
     }
-    const long long blocks = (long long)p.works * p.splits * p.Hkv;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const long long items = (long long)p.works * p.splits * p.Hkv;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned blocks = (unsigned)std::min<long long>(items, sm_count());
     e = f8 ? prepare<true>() : prepare<false>();
     if (e != cudaSuccess) return e;
-    if (f8) ragged_attn_tc<true><<<(unsigned)blocks, Ring<true>::threads, kRaggedSmem, st>>>(mq, mk, mv, p);
-    else ragged_attn_tc<false><<<(unsigned)blocks, Ring<false>::threads, kRaggedSmem, st>>>(mq, mk, mv, p);
+    if (f8) ragged_attn_tc<true><<<blocks, Ring<true>::threads, kRaggedSmem, st>>>(mq, mk, mv, p);
+    else ragged_attn_tc<false><<<blocks, Ring<false>::threads, kRaggedSmem, st>>>(mq, mk, mv, p);
     count_launch();
     e = cudaGetLastError();
     return e == cudaSuccess ? combine_launch(p, st) : e;
