@@ -23,19 +23,18 @@
 //   0-3, 4-7  softmax warpgroups, thread = row
 //   8         TMA producer (Q once; K and V tiles, or the pages that make one
 //             up, in the order the MMAs consume them)
-//   9         MMA issuer (one thread)
-//   10        zeroes the value rows behind a sequence's end (whatever lies
-//             there, NaN included, would reach the output as 0 * NaN)
+//   9, 10     MMA issuers of row tile 0 and 1
 //   11        finds the items, two ahead
 //   12-15     8-bit caches only: widen staged rows to bf16 tiles.  A code
 //             times a power of two is a bf16 number, so nothing is rounded.
-// TMEM (512 columns): S0 | S1 | O0 | O1.  P overwrites its S tile (64 of 128
-// columns) and is the MMA's A operand there: with both operands in shared
-// memory, Q K^T and P V of 128 keys read 128 bytes a clock, all that shared
-// memory has, and writing P there too would add a quarter; from TMEM the P V
-// products read V only.  The two tiles alternate on the tensor cores: one's
-// softmax runs under the other's products.  P is handed over in two halves,
-// so that the first half's product runs under the second half's exponentials.
+// TMEM (512 columns): two S buffers of 64 keys for each row tile, then O0 and
+// O1.  A key tile is taken in two steps of 64 keys, so that S of the next step
+// is computed while the softmax of this one runs: with one 128-key S per row
+// tile the softmax would wait for P V and the next Q K^T each time (measured
+// 4300 clocks a pair of tiles against 2048 of products).  P overwrites its S
+// buffer and is the MMA's A operand there: P in shared memory would add its
+// writes and reads to an operand traffic that already fills the 128 bytes a
+// clock (64-key Q K^T: 48 KB in 256 clocks of products).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -87,11 +86,12 @@ struct RaggedBars {
     uint64_t q_full, q_empty;             // q_empty: the MMAs have read Q (commit), and a warpgroup has no use for its place
     uint64_t kv_full[5], kv_empty[5];
     uint64_t st_full[4], st_empty[4];     // staged 8-bit tiles
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];
+    uint64_t s_full[2][2], p_full[2][2];  // of each S buffer
+    uint64_t pv_done[2];                  // each step's P V
+    uint64_t o_full[2], o_empty[2];       // an item's last P V; O read out
     uint64_t work_full[2], work_empty[2];
-    uint64_t vgo, vfix;                   // last value tile: there / its rows behind the end zeroed
     uint64_t side_full;                   // solo: warpgroup 1's half is in shared memory
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     uint32_t bad_any[kBadBufs];           // K tile i of the CTA has keys on pages outside the pool: bad[i % 8] says which
@@ -342,6 +342,23 @@ __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t leader) {
         : "memory");
 }
 
+// mbar_wait whose first poll does not suspend the thread: with a limit of 0
+// it gives up whenever the phase is not complete yet.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort) {
+    uint32_t there;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(there)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (there) return true;
+    if (limit_ns == 0) {
+        *abort = 1;
+        return false;
+    }
+    return mbar_wait(bar, parity, limit_ns, abort);
+}
+
 // A count of uses whose parity a barrier's waits follow.
 struct Phase {
     uint32_t n = 0;
@@ -373,7 +390,7 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
 
 // Of every 8 pairs of probabilities in a tile without masked keys, how many
 // come from exp2_fma.
-constexpr int kFmaPairs = 3;
+constexpr int kFmaPairs = 2;
 
 template <bool F8>
 __global__ void __launch_bounds__(Ring<F8>::threads, 1)
@@ -392,28 +409,29 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     constexpr int readers = F8 ? 15 : 11;      // warps that read each work item (all but the one that finds it)
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->q_full), 1);
-        mbar_init(smem_u32(&bars->q_empty), 1 + 128);
+        mbar_init(smem_u32(&bars->q_empty), 2 + 128);
         for (int s = 0; s < 5; ++s) {
             mbar_init(smem_u32(&bars->kv_full[s]), F8 ? 128 : 1);
-            mbar_init(smem_u32(&bars->kv_empty[s]), 1);
+            mbar_init(smem_u32(&bars->kv_empty[s]), 2);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(smem_u32(&bars->st_full[s]), 1);
             mbar_init(smem_u32(&bars->st_empty[s]), 128);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(smem_u32(&bars->s_full[w]), 1);
-            mbar_init(smem_u32(&bars->p_full[w][0]), 128);
-            mbar_init(smem_u32(&bars->p_full[w][1]), 128);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&bars->s_full[w][b]), 1);
+                mbar_init(smem_u32(&bars->p_full[w][b]), 128);
+            }
+            mbar_init(smem_u32(&bars->pv_done[w]), 1);
             mbar_init(smem_u32(&bars->o_full[w]), 1);
             mbar_init(smem_u32(&bars->o_empty[w]), 128);
             mbar_init(smem_u32(&bars->work_full[w]), 1);
             mbar_init(smem_u32(&bars->work_empty[w]), readers);
         }
-        mbar_init(smem_u32(&bars->vgo), 1);
-        mbar_init(smem_u32(&bars->vfix), 32);
         mbar_init(smem_u32(&bars->side_full), 128);
-        mbar_init(smem_u32(&bars->drain), 1);
+        mbar_init(smem_u32(&bars->drain[0]), 1);
+        mbar_init(smem_u32(&bars->drain[1]), 1);
         bars->abort = 0;
         fence_mbar_init();
     }
@@ -438,7 +456,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     Work wk;
     auto next_work = [&]() -> bool {
         const int slot = work_i & 1;
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->work_full[slot]), (work_i >> 1) & 1, p.wait_ns,
+        const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->work_full[slot]), (work_i >> 1) & 1, p.wait_ns,
                                                           abort));
         if (!ok) return false;
         wk = bars->work[slot];
@@ -456,7 +474,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             // ------------------------------------------------ items
             for (int i = 0;; ++i) {
                 const Work w = find_work(p, i);
-                const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->work_empty[i & 1]), ((i >> 1) & 1) ^ 1,
+                const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->work_empty[i & 1]), ((i >> 1) & 1) ^ 1,
                                                                   p.wait_ns, abort));
                 if (!ok) break;
                 if (lane == 0) {
@@ -482,7 +500,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             while (ok && next_work()) {
                 const int n = wk.n;
                 if (n == 0) continue;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_empty), q_free.take_free(), p.wait_ns, abort));
+                ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->q_empty), q_free.take_free(), p.wait_ns, abort));
                 if (!ok) break;
                 const bool solo = wk.solo != 0;
                 if (lane == 0) {
@@ -503,7 +521,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const int boxes = p.paged ? (min(BN, wk.kvl - key0) + p.box_rows - 1) >> rshift : 1;
                     int page = 0;
                     if (p.paged && lane < boxes) page = __ldg(table + ((key0 + (lane << rshift)) >> p.c.page_shift));
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[pos.slot]), pos.phase ^ 1, p.wait_ns, abort));
+                    ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&empty[pos.slot]), pos.phase ^ 1, p.wait_ns, abort));
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[pos.slot]);
                     const uint32_t dst = smem_u32(F8 ? sst + pos.slot * kStage : skv + pos.slot * TILE);
@@ -548,20 +566,22 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 for (uint32_t it = issued > (uint32_t)slots ? issued - slots : 0; it < issued; ++it)
                     mbar_drain(smem_u32(&full[it % slots]), (it / slots) & 1);
             }
-        } else if (warp == 9) {
-            // ------------------------------------------------ MMA issuer
+        } else if (warp == 9 || warp == 10) {
+            // ------------------------------------------------ MMA issuers, one for each row tile
             // The whole warp goes through the loop and one elected lane issues, so
-            // that descriptors stay in uniform registers: built in a single thread's
-            // branch they cost more than the products they start.
+            // that descriptors stay in uniform registers.  Two issuers, because one
+            // spent as long on its waits and commits between the two row tiles'
+            // chains as the products took.
+            const int w = warp - 9;
             const uint32_t leader = elect_one();
-            const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
-            const uint32_t q_lo[2] = {desc_lo(smem_u32(sq)), desc_lo(smem_u32(sq + TILE))};
+            const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
             const uint32_t kv_lo = desc_lo(smem_u32(skv));
-            Phase q_phase, o_free[2], p_phase[2], fix_phase;
+            Phase q_phase, o_free;
+            uint32_t p_uses = 0;                       // P handed over so far: buffer = the last bit
             RingPos pos;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.wait_ns, abort));
+                ok = ok && __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, p.wait_ns, abort));
                 if (ok) tc_fence_after();
                 return ok;
             };
@@ -569,142 +589,135 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const int n = __shfl_sync(0xffffffffu, wk.n, 0);
                 if (n == 0) continue;
                 const bool solo = __shfl_sync(0xffffffffu, wk.solo, 0) != 0;
-                const int n0 = __shfl_sync(0xffffffffu, wk.n0, 0), n1 = __shfl_sync(0xffffffffu, wk.n1, 0);
-                const bool fix = !F8 && __shfl_sync(0xffffffffu, tail_rows(), 0) < BN;
-                int done0 = 0, done1 = 0;
-                const uint32_t q1_lo = solo ? q_lo[0] : q_lo[1];
-                // S_w = Q_w K^T, K in the ring's current slot
-                auto qk = [&](auto w_) {
-                    constexpr int w = decltype(w_)::value;
-                    const uint32_t a = w == 0 ? q_lo[0] : q1_lo, b = kv_lo + pos.slot * (TILE >> 4);
-                    constexpr uint32_t I = idesc_bf16(128, 128, false, false);
+                const int nw = __shfl_sync(0xffffffffu, w == 0 ? wk.n0 : wk.n1, 0);
+                const int tail = __shfl_sync(0xffffffffu, tail_rows(), 0);
+                const uint32_t q_lo = desc_lo(smem_u32(solo ? sq : sq + w * TILE));
+                uint32_t begun = 0;                    // O has been written by this item
+                int left = 2 * nw;
+                // S = Q K^T for half h of the key tile in ring slot `slot` (buffer h)
+                auto qk = [&](int slot, int h) {
+                    const uint32_t b = kv_lo + slot * (TILE >> 4) + h * ((64 * 128) >> 4);
+                    constexpr uint32_t I = idesc_bf16(128, 64, false, false);
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
                         const uint32_t o = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                        mma_ss_one(tS[w], a + o, b + o, kDescHi, kDescHi, I, kk > 0 ? 1u : 0u, leader);
+                        mma_ss_one(tS + h * 64, q_lo + o, b + o, kDescHi, kDescHi, I, kk > 0 ? 1u : 0u, leader);
                     }
-                    commit_one(smem_u32(&bars->s_full[w]), leader);
+                    commit_one(smem_u32(&bars->s_full[w][h]), leader);
                 };
-                // O_w += P_w V, half by half as P arrives
-                auto pv = [&](auto w_, int slot, int &done, int all) {
-                    constexpr int w = decltype(w_)::value;
+                // O += P V for half h of the value tile in ring slot `slot`
+                auto pv = [&](int slot, int h) {
                     constexpr uint32_t I = idesc_bf16(128, 128, false, true);
-                    const uint32_t parity = p_phase[w].take();
-                    const uint32_t b = kv_lo + slot * (TILE >> 4);
+                    if (!wait(&bars->p_full[w][h], (p_uses >> 1) & 1)) return false;
+                    ++p_uses;
+                    const uint32_t b = kv_lo + slot * (TILE >> 4) + h * ((64 * 128) >> 4) + (kDescLboV << 16);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!wait(&bars->p_full[w][half], parity)) return;
-#pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            mma_ts_one(tO[w], tS[w] + kk * 8, b + ((kk * 2048) >> 4) + (kDescLboV << 16), kDescHi, I,
-                                       (kk > 0 || done > 0) ? 1u : 0u, leader);
-                    }
-                    if (++done == all) commit_one(smem_u32(&bars->o_full[w]), leader);
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts_one(tO, tS + h * 64 + kk * 8, b + ((kk * 2048) >> 4), kDescHi, I, kk > 0 ? 1u : begun,
+                                   leader);
+                    begun = 1;
+                    commit_one(smem_u32(&bars->pv_done[w]), leader);
+                    if (--left == 0) commit_one(smem_u32(&bars->o_full[w]), leader);
+                    return true;
                 };
-                constexpr std::integral_constant<int, 0> W0{};
-                constexpr std::integral_constant<int, 1> W1{};
-                // the last value tile may have rows to be zeroed first
-                auto tail_wait = [&](int j) {
-                    if (fix && j == n - 1) {
-                        if (leader) mbar_arrive(smem_u32(&bars->vgo));
-                        wait(&bars->vfix, fix_phase.take());
+                // Zero the value rows behind the sequence's end, in the last tile: whatever
+                // lies there, NaN included, would reach the output as 0 * NaN.  (Both
+                // issuers may do it to the same tile.)  Whole 128-byte rows, so the
+                // swizzle within a row does not matter.
+                auto zero_tail = [&](int slot, int j) {
+                    if constexpr (!F8) {
+                        if (j != n - 1 || tail >= BN) return;
+                        for (int i = lane; i < (BN - tail) * 16; i += 32) {
+                            const int row = tail + (i >> 4), part = i & 15;
+                            *reinterpret_cast<uint4 *>(skv + slot * TILE + (part >> 3) * HALF + row * 128 +
+                                                       (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    return ok;
                 };
-                auto release = [&](int slot) { commit_one(smem_u32(&bars->kv_empty[slot]), leader); };
                 auto kv_wait = [&]() { return wait(&bars->kv_full[pos.slot], pos.phase); };
-                if (!wait(&bars->q_full, q_phase.take()) || !kv_wait()) break;
+                auto take_slot = [&]() {
+                    const int slot = pos.slot;
+                    pos.next(R::slots);
+                    return slot;
+                };
+                // a slot is free after two commits: both issuers', or both of the only one that uses it
+                auto release = [&](int slot, bool alone) {
+                    commit_one(smem_u32(&bars->kv_empty[slot]), leader);
+                    if (alone) commit_one(smem_u32(&bars->kv_empty[slot]), leader);
+                };
+                if (!wait(&bars->q_full, q_phase.take())) break;
+                // First both steps of the row tile's first key tile; then, step by step, P V
+                // and the same step of its next key tile's Q K^T, which may overwrite S as
+                // soon as that P has been read.
                 if (!solo) {
-                    if (n0 > 0) qk(W0);
-                    qk(W1);
-                    release(pos.slot);
-                    pos.next(R::slots);
-                    if (n == 1) commit_one(smem_u32(&bars->q_empty), leader);
-                } else {
-                    qk(W0);
-                    release(pos.slot);
-                    pos.next(R::slots);
-                    if (n > 1) {
-                        if (!kv_wait()) break;
-                        qk(W1);
-                        release(pos.slot);
-                        pos.next(R::slots);
+                    if (!kv_wait()) break;
+                    const int slot = take_slot();
+                    if (nw > 0) {
+                        qk(slot, 0);
+                        qk(slot, 1);
                     }
-                    if (n <= 2) commit_one(smem_u32(&bars->q_empty), leader);
+                    release(slot, false);
+                } else {
+                    // (the first two K tiles are row tile 0's and 1's; each issuer waits for
+                    // the other's tiles too, or it would lose count of the slots' phases)
+                    for (int j = 0; j < min(n, 2); ++j) {
+                        if (!kv_wait()) break;
+                        const int slot = take_slot();
+                        if (j != w) continue;
+                        qk(slot, 0);
+                        qk(slot, 1);
+                        release(slot, true);
+                    }
                 }
+                if (nw <= 1) commit_one(smem_u32(&bars->q_empty), leader);       // the last product with Q
                 // O may be overwritten once the item that had it before has been read out
-                if (n0 > 0 && !wait(&bars->o_empty[0], o_free[0].take_free())) break;
-                if (n1 > 0 && !wait(&bars->o_empty[1], o_free[1].take_free())) break;
-                if (!solo) {
-                    for (int j = 0; j < n; ++j) {          // n1 = n >= n0
-                        if (!kv_wait() || !tail_wait(j)) break;
-                        const int v_slot = pos.slot;
-                        pos.next(R::slots);
-                        const bool more = j + 1 < n;
-                        if (j < n0) {
-                            pv(W0, v_slot, done0, n0);
-                            if (!ok) break;
-                            if (j + 1 < n0) {
-                                if (!kv_wait()) break;
-                                qk(W0);
+                if (nw > 0 && !wait(&bars->o_empty[w], o_free.take_free())) break;
+                int done = 0;                          // key tiles of this row tile
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool mine = solo ? (j & 1) == w : j < nw;
+                    const bool k_there = j + (solo ? 2 : 1) < n;       // a K tile follows V_j in the ring
+                    if (!kv_wait()) break;
+                    const int v = take_slot();
+                    if (solo && !mine) {
+                        if (k_there) {
+                            if (!kv_wait()) break;
+                            take_slot();
+                        }
+                        continue;
+                    }
+                    int k = -1;
+                    if (mine) {
+                        zero_tail(v, j);
+                        ++done;
+                        for (int h = 0; h < 2; ++h) {
+                            if (!pv(v, h)) break;
+                            if (done < nw) {
+                                if (k < 0) {
+                                    if (!kv_wait()) break;
+                                    k = take_slot();
+                                }
+                                qk(k, h);
                             }
                         }
-                        pv(W1, v_slot, done1, n1);
                         if (!ok) break;
-                        release(v_slot);
-                        if (more) {
-                            if (!kv_wait()) break;
-                            qk(W1);
-                            release(pos.slot);
-                            pos.next(R::slots);
-                            if (j + 2 == n) commit_one(smem_u32(&bars->q_empty), leader);   // the last product with Q
-                        }
+                        if (done + 1 == nw) commit_one(smem_u32(&bars->q_empty), leader);
                     }
-                } else {
-                    for (int j = 0; j < n; ++j) {
-                        if (!kv_wait() || !tail_wait(j)) break;
-                        if (j & 1) pv(W1, pos.slot, done1, n1);
-                        else pv(W0, pos.slot, done0, n0);
-                        if (!ok) break;
-                        release(pos.slot);
-                        pos.next(R::slots);
-                        if (j + 2 < n) {
+                    release(v, solo);
+                    if (k_there) {
+                        if (k < 0) {                   // not needed here, but there to be released
                             if (!kv_wait()) break;
-                            if (j & 1) qk(W1);
-                            else qk(W0);
-                            release(pos.slot);
-                            pos.next(R::slots);
-                            if (j + 3 == n) commit_one(smem_u32(&bars->q_empty), leader);
+                            k = take_slot();
                         }
+                        release(k, solo);
                     }
                 }
             }
             // all MMAs this warp issued have completed before TMEM is freed
-            commit_one(smem_u32(&bars->drain), leader);
-            if (leader) mbar_drain(smem_u32(&bars->drain), 0);
+            commit_one(smem_u32(&bars->drain[w]), leader);
+            if (leader) mbar_drain(smem_u32(&bars->drain[w]), 0);
             __syncwarp();
-        } else if (warp == 10) {
-            // ------------------------------------------------ value rows behind the end
-            Phase go;
-            uint32_t items = 0;     // K and V tiles before this item
-            while (next_work()) {
-                const int tail = tail_rows();
-                if (!F8 && wk.n > 0 && tail < BN) {
-                    // (the MMA thread, which has waited for the tile, says when)
-                    const int slot = (items + 2 * wk.n - 1) % R::slots;
-                    const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->vgo), go.take(), p.wait_ns, abort));
-                    if (!ok) break;
-                    // whole 128-byte rows, so the swizzle within a row does not matter
-                    for (int i = lane; i < (BN - tail) * 16; i += 32) {
-                        const int row = tail + (i >> 4), part = i & 15;
-                        *reinterpret_cast<uint4 *>(skv + slot * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&bars->vfix));
-                }
-                items += 2 * wk.n;
-            }
         } else if (F8) {
             // ------------------------------------------------ 8-bit rows to bf16 tiles
             const int t = threadIdx.x - 384;
@@ -742,8 +755,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const int buf = tiles & 1;
                     bars->scale[buf][t] = (uint8_t)byte;
                     byte = scale_load(it + 1);
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->st_full[st.slot]), st.phase, p.wait_ns, abort));
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_empty[kv.slot]), kv.phase ^ 1,
+                    ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->st_full[st.slot]), st.phase, p.wait_ns, abort));
+                    ok = ok && __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->kv_empty[kv.slot]), kv.phase ^ 1,
                                                                  p.wait_ns, abort));
                     // the four warps meet here for the scale bytes, and leave together when
                     // one of them gave up waiting
@@ -793,7 +806,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const float c2 = p.scale_log2;
         const float nan = __int_as_float(0x7fc00000);
         const int row_tok = tw / p.G, row_head = tw - row_tok * p.G;
-        Phase s_phase, o_phase, side_phase;
+        Phase side_phase, o_phase;
+        uint32_t steps_done = 0;       // steps of 64 keys so far: the buffer and the parities follow
         uint32_t k_tiles = 0;
         bool ok = true;
         while (ok && next_work()) {
@@ -807,36 +821,37 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const int nw = w == 0 ? wk.n0 : wk.n1;
             const bool join = solo && n > 1;
             float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < nw; ++i) {
-                const int j = solo ? 2 * i + w : i;
-                const int key0 = (wk.j0 + j) * BN;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[w]), s_phase.take(), p.wait_ns, abort));
+            for (int u = 0; u < 2 * nw; ++u, ++steps_done) {
+                const int buf = steps_done & 1;             // = u & 1: half of the key tile
+                const int j = solo ? (u & ~1) + w : u >> 1;
+                const int key0 = (wk.j0 + j) * BN + buf * 64;
+                ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->s_full[w][buf]), (steps_done >> 1) & 1, p.wait_ns,
+                                                       abort));
                 if (!ok) break;
                 tc_fence_after();
                 // Q's place is only needed here again when the halves are joined there
                 // (then warpgroup 0 says when it is done with it)
-                if (i == 0 && !join && w == (solo ? 0 : 1)) mbar_arrive(smem_u32(&bars->q_empty));
-                // S_i is there, and P V of the previous tile (issued before it) is done
-                float s[128];
+                if (u == 0 && !join && w == (solo ? 0 : 1)) mbar_arrive(smem_u32(&bars->q_empty));
+                float s[64];
                 {
-                    uint32_t r[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
+                    uint32_t r[2][32];
+                    tmem_ld32(tS + buf * 64, r[0]);
+                    tmem_ld32(tS + buf * 64 + 32, r[1]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(r[c >> 5][c & 31]);
+                    for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(r[c >> 5][c & 31]);
                 }
                 const int bad = (k_tiles + j) % kBadBufs;
                 const bool lost = p.paged && bars->bad_any[bad] != 0;
-                const bool masked = lost || key0 + BN - 1 > pos_first;
+                const bool masked = lost || key0 + 63 > pos_first;
                 if (masked) {
                     // one bit a key: up to the row's own position, and not on a lost page
                     const int seen = pos - key0 + 1;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         const int k = min(max(seen - 32 * q, 0), 32);
                         uint32_t bits = k == 32 ? 0xffffffffu : (1u << k) - 1u;
-                        if (lost) bits &= ~bars->bad[bad][q];
+                        if (lost) bits &= ~bars->bad[bad][2 * buf + q];
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (!((bits >> c) & 1u)) s[32 * q + c] = -INFINITY;
@@ -844,13 +859,21 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int c = 4; c < 128; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+                for (int c = 4; c < 64; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
                 const float mx2 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
                 // the running maximum only moves when it grows by more than 8 (log2
                 // units); the final division uses the same reference
                 if (__any_sync(0xffffffffu, mx2 > m + 8.0f)) {
                     const float m_new = fmaxf(m, mx2);
-                    if (i > 0) {
+                    if (u > 0) {
+                        // The product of the step before has to be in O first.  (Its phase is
+                        // the barrier's last or current one: the step before that is done,
+                        // since this step's S was computed after it, and this one's P is not
+                        // handed over yet.)
+                        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->pv_done[w]), (steps_done - 1) & 1, p.wait_ns,
+                                                               abort));
+                        if (!ok) break;
+                        tc_fence_after();
                         const float corr = m_new == -INFINITY ? 1.f : ex2(m - m_new);
                         l *= corr;
 #pragma unroll 1
@@ -869,10 +892,9 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const float mref = m == -INFINITY ? 0.f : m;   // masked keys (-inf) give 2^-inf = 0
                 const float2 c2v = make_float2(c2, c2), mv = make_float2(-mref, -mref);
                 float2 ps01 = make_float2(0.f, 0.f), ps23 = make_float2(0.f, 0.f);
-                // 64 keys to P: every 16 columns of bf16 pairs leave as soon as they are done
-                auto probabilities = [&](int half, auto fma_pairs) {
+                auto probabilities = [&](auto fma_pairs) {
 #pragma unroll
-                    for (int ch = 2 * half; ch < 2 * half + 2; ++ch) {
+                    for (int ch = 0; ch < 2; ++ch) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -884,24 +906,19 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                             // P is rounded to bf16, the type of V: one MMA takes one type
                             pk[e] = pack_bf16(ab.x, ab.y);
                         }
-                        tmem_st16(tS + 16 * ch, pk);
+                        tmem_st16(tS + buf * 64 + 16 * ch, pk);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(&bars->p_full[w][half]));
                 };
-                if (masked) {          // exp2_fma would not give 0 for a masked key
-                    probabilities(0, std::integral_constant<int, 0>());
-                    probabilities(1, std::integral_constant<int, 0>());
-                } else {
-                    probabilities(0, std::integral_constant<int, kFmaPairs>());
-                    probabilities(1, std::integral_constant<int, kFmaPairs>());
-                }
+                if (masked) probabilities(std::integral_constant<int, 0>());   // exp2_fma would not give 0 for a masked key
+                else probabilities(std::integral_constant<int, kFmaPairs>());
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&bars->p_full[w][buf]));
                 l += (ps01.x + ps01.y) + (ps23.x + ps23.y);
             }
             k_tiles += n;
             if (nw > 0)
-                ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&bars->o_full[w]), o_phase.take(), p.wait_ns, abort));
+                ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(&bars->o_full[w]), o_phase.take(), p.wait_ns, abort));
             bool fin = ok;
             tc_fence_after();
             // O of this thread's row: columns [16 c, 16 c + 16), zeros when there were no tiles
@@ -934,7 +951,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     fence_proxy_async_smem();      // the next Q tiles come here through the async proxy
                     mbar_arrive(smem_u32(&bars->side_full));
                 } else {
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->side_full), side_phase.take(), p.wait_ns, abort));
+                    ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->side_full), side_phase.take(), p.wait_ns, abort));
                     if (!ok) fin = false;
                     const float2 other = bars->side[tw];
                     const float top = fmaxf(m, other.x);
