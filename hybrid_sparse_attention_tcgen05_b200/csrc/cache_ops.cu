@@ -132,9 +132,10 @@ template <typename T, int V, bool INTER>
 cudaError_t rope_go(RopeParams p, bool copy_rest, cudaStream_t st) {
     p.units = INTER ? (copy_rest ? p.d : 2 * p.half) / V : (copy_rest ? p.d - p.half : p.half) / V;
     const long long per_token = (long long)(p.Hq + p.Hkv) * p.units;
-    // one token a block while that leaves SMs idle, then four: fewer blocks,
-    // and the angles of four tokens fill the block's threads
-    p.tokens = p.T >= 4096 ? 4 : 1;
+    // one token a block while that leaves SMs idle, then eight: fewer blocks,
+    // and the angles of eight tokens fill the block's threads (65536 tokens of
+    // 68 heads: two 477 us, four 429, eight 416)
+    p.tokens = p.T >= 4096 ? 8 : 1;
     const int blocks = (p.T + p.tokens - 1) / p.tokens;
     const long long n = per_token * p.tokens;
     int y = (int)((n + 2 * kThreads - 1) / (2 * kThreads));
@@ -165,6 +166,8 @@ cudaError_t rope_typed(const RopeParams &p, bool interleaved, bool copy_rest, cu
 struct WriteParams {
     PagedCache c;
     int T, Hkv, d, half;          // half: rotated pairs of a key (0: none)
+    int cs_ld;                     // floats of cosines and sines for each token
+    int group_shift, dq, dr;       // lanes of a row (log2); tokens and heads that a block's rows advance by
     long long ld_k, ld_v;
     const void *k, *v;
     const double *inv_freq;
@@ -174,19 +177,49 @@ struct WriteParams {
     int tokens;                    // tokens a block takes
 };
 
-// Eight elements of a row from element e0 on, rotated when they lie in the
-// rotated part (d and e0 are multiples of 8).  The partners of the first half
-// lie `half` further, those of the second half `half` back; they come from
-// the row just read (L1).
+// Eight neighbouring elements of a row as they lie in memory.
+template <typename T> struct Raw8 {
+    uint4 q[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void widen(float (&x)[8]) const {
+        const T *e = reinterpret_cast<const T *>(q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = Elem<T>::to_f(e[i]);
+    }
+    __device__ __forceinline__ Raw8 shuffle(int src) const {
+        Raw8 r;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            r.q[i].x = __shfl_sync(0xffffffffu, q[i].x, src);
+            r.q[i].y = __shfl_sync(0xffffffffu, q[i].y, src);
+            r.q[i].z = __shfl_sync(0xffffffffu, q[i].z, src);
+            r.q[i].w = __shfl_sync(0xffffffffu, q[i].w, src);
+        }
+        return r;
+    }
+};
+
+// The rotated part of elements e0 .. e0 + 7 (d and e0 are multiples of 8) of
+// a key row, x, turned in place.  cs: cosines, sines and negative sines of
+// the token's pairs, half of each.  y: the elements half further or half back, when half is
+// a multiple of 8 (they are another lane's); otherwise `row` is read again.
 template <typename T>
-__device__ __forceinline__ void load_row8(const T *row, int e0, int half, bool inter, const float2 *cs, float (&x)[8]) {
-    load_n<8>(row + e0, x);
+__device__ __forceinline__ void turn8(float (&x)[8], const float (&y)[8], const T *row, int e0, int half, bool inter,
+                                      const float *cs) {
     if (e0 >= 2 * half) return;
+    const float *sn = cs + half;
     if (inter) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             if (e0 + i < 2 * half) {
-                const float2 w = cs[(e0 + i) / 2];
+                const float2 w = make_float2(cs[(e0 + i) / 2], sn[(e0 + i) / 2]);
                 const float a = x[i], b = x[i + 1];
                 x[i] = rope_first(a, b, w);
                 x[i + 1] = rope_second(a, b, w);
@@ -195,19 +228,26 @@ __device__ __forceinline__ void load_row8(const T *row, int e0, int half, bool i
         return;
     }
     if ((half & 7) == 0) {
+        // the first half's x cos - y sin is x cos + y (-sin), and the negative
+        // sines lie after the sines: no lane has to choose
         const bool first = e0 < half;
-        float y[8];
-        load_n<8>(row + (first ? e0 + half : e0 - half), y);
-        const float2 *w = cs + (first ? e0 : e0 - half);
+        const int p0 = first ? e0 : e0 - half;
+        const float *sg = sn + (first ? half : 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = first ? rope_first(x[i], y[i], w[i]) : rope_second(y[i], x[i], w[i]);
+        for (int i = 0; i < 8; i += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(cs + p0 + i), s = *reinterpret_cast<const float4 *>(sg + p0 + i);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i + k] = rope_second(y[i + k], x[i + k], make_float2(cc[k], ss[k]));
+        }
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int e = e0 + i;
-        if (e < half) x[i] = rope_first(x[i], Elem<T>::to_f(row[e + half]), cs[e]);
-        else if (e < 2 * half) x[i] = rope_second(Elem<T>::to_f(row[e - half]), x[i], cs[e - half]);
+        if (e < half) x[i] = rope_first(x[i], Elem<T>::to_f(row[e + half]), make_float2(cs[e], sn[e]));
+        else if (e < 2 * half)
+            x[i] = rope_second(Elem<T>::to_f(row[e - half]), x[i], make_float2(cs[e - half], sn[e - half]));
     }
 }
 
@@ -222,90 +262,152 @@ __device__ __forceinline__ int scale_byte(float amax) {
     return e < 1 ? 1 : e;
 }
 
+constexpr int kBatch = 4;          // rows a thread of the write has in flight
+constexpr int kWriteTokens = 8;    // most tokens a block of it takes
+
 // One group of lanes per (token, K or V, head) row, eight elements a lane.
 // 8-bit rows: the group's largest magnitude gives the scale, a power of two,
 // so that dividing by it is exact and the 8-bit float is the only rounding
 // (by at most 2^-4 of the value); every reader can widen such a value to bf16
 // exactly.
+//
+// The rows themselves are asked for first, kBatch of them a thread: the
+// places of the tokens (three dependent loads) and the angles (64-bit
+// arithmetic) are found while they come.
 template <typename TI, typename TO, bool Q8>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams p) {
-    extern __shared__ float2 cs[];
-    __shared__ long long slot[8];
+__global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const WriteParams p) {
+    extern __shared__ __align__(16) float wcs[];   // per token: cosines, sines, negative sines
+    __shared__ size_t data_at[kWriteTokens];       // the token's place in the pools, in elements
+    __shared__ size_t scale_at[kWriteTokens];      // and its first head's scale
+    __shared__ int at[kWriteTokens];               // its position; < 0: it has no place
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * p.tokens;
-    const int nt = min(p.tokens, p.T - t0);        // tokens <= 8: one warp finds each token's place
-    __shared__ int at[8];
-    if (warp < nt) {
+    const int nt = min(p.tokens, p.T - t0);
+    const int lanes = p.d / 8;                     // lanes that hold a row, of a group of 2^group_shift
+    const int group = 1 << p.group_shift;
+    const int sub = threadIdx.x & (group - 1);
+    const int per = kThreads >> p.group_shift;     // rows a block handles at a time
+    const int heads = 2 * p.Hkv;                   // rows of a token: K heads, then V heads
+    const TI *const kb = (const TI *)p.k + (long long)t0 * p.ld_k + sub * 8;
+    const TI *const vb = (const TI *)p.v + (long long)t0 * p.ld_v + sub * 8;
+    // this thread's next row, as token and head of the block: one division,
+    // then steps of `per` rows (dq tokens and dr heads)
+    struct Row {
+        int tok, kh;
+        __device__ __forceinline__ void next(const WriteParams &p, int heads) {
+            tok += p.dq;
+            kh += p.dr;
+            if (kh >= heads) {
+                kh -= heads;
+                ++tok;
+            }
+        }
+    };
+    Row asked;
+    asked.tok = (int)(threadIdx.x >> p.group_shift) / heads;
+    asked.kh = (int)(threadIdx.x >> p.group_shift) - asked.tok * heads;
+    Row row = asked;
+    Raw8<TI> raw[kBatch];
+    auto ask = [&]() {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (asked.tok < nt && sub < lanes)
+                raw[u].load(asked.kh >= p.Hkv ? vb + asked.tok * p.ld_v + (asked.kh - p.Hkv) * p.d
+                                              : kb + asked.tok * p.ld_k + asked.kh * p.d);
+            else raw[u].zero();
+            asked.next(p, heads);
+        }
+    };
+    ask();
+    if (warp < nt) {                               // one warp finds each token's place
         int b = 0;
         const long long pos = cache_position(p.c, p.T, t0 + warp, p.status, &b);
         const long long r = pos < 0 ? -1 : pool_row(p.c, b, pos, p.status);
         if (lane == 0) {
-            slot[warp] = r;
-            at[warp] = (int)pos;
+            at[warp] = r < 0 ? -1 : (int)pos;
+            data_at[warp] = r < 0 ? 0 : (size_t)r * p.Hkv * p.d;
+            scale_at[warp] = r < 0 ? 0 : scale_index(p.c, r, p.Hkv, 0);
         }
     }
     __syncthreads();
     if (p.half > 0) {
-        for (int i = threadIdx.x; i < nt * p.half; i += kThreads)
-            if (slot[i / p.half] >= 0) cs[i] = rope_cs(at[i / p.half], p.inv_freq[i % p.half], p.amp);
+        for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
+            const int tok = i / p.half, pair = i - tok * p.half;
+            if (at[tok] >= 0) {
+                const float2 w = rope_cs(at[tok], p.inv_freq[pair], p.amp);
+                wcs[tok * p.cs_ld + pair] = w.x;
+                wcs[tok * p.cs_ld + p.half + pair] = w.y;
+                wcs[tok * p.cs_ld + 2 * p.half + pair] = -w.y;
+            }
+        }
         __syncthreads();
     }
-    const int lanes = p.d / 8;                                    // lanes that hold the row
-    const int group = lanes <= 1 ? 1 : 1 << (32 - __clz(lanes - 1));   // rounded up to a power of two (<= 32)
-    const int sub = threadIdx.x & (group - 1);
-    const int per = kThreads / group;                             // rows a block handles at a time
-    const int rows = nt * 2 * p.Hkv;
-    for (int r0 = 0; r0 < rows; r0 += per) {
-        const int r = r0 + threadIdx.x / group;
-        const int tok = r / (2 * p.Hkv);
-        const int kh = r - tok * 2 * p.Hkv;
-        const bool is_v = kh >= p.Hkv;
-        const int h = is_v ? kh - p.Hkv : kh;
-        const bool live = r < rows && sub < lanes && slot[min(tok, nt - 1)] >= 0;
-        float x[8];
-        if (live) {
-            const TI *row = is_v ? (const TI *)p.v + (long long)(t0 + tok) * p.ld_v + h * p.d
-                                 : (const TI *)p.k + (long long)(t0 + tok) * p.ld_k + h * p.d;
-            load_row8(row, sub * 8, is_v ? 0 : p.half, p.interleaved != 0, cs + tok * p.half, x);
-        } else {
+    const int passes = (nt * heads + per - 1) >> (8 - p.group_shift);      // per = 2^(8 - group_shift)
+    for (int i0 = 0; i0 < passes; i0 += kBatch) {
+        if (i0 > 0) ask();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        }
-        [[maybe_unused]] int byte = 127;
-        if constexpr (Q8) {
-            float m = 0.f;
+        for (int u = 0; u < kBatch; ++u) {
+            if (i0 + u >= passes) break;                               // (the same for the whole block)
+            const int tok = min(row.tok, nt - 1), kh = row.kh;
+            const bool is_v = kh >= p.Hkv;
+            const bool live = row.tok < nt && sub < lanes && at[tok] >= 0;
+            row.next(p, heads);
+            float x[8];
+            raw[u].widen(x);
+            if (p.half > 0 && __any_sync(0xffffffffu, live && !is_v)) {
+                float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (!p.interleaved && (p.half & 7) == 0) {             // the partners are another lane's
+                    const int hl = p.half / 8;
+                    raw[u].shuffle((lane & ~(group - 1)) + (sub < hl ? sub + hl : max(sub - hl, 0))).widen(y);
+                }
+                if (live && !is_v)
+                    turn8(x, y, kb - sub * 8 + tok * p.ld_k + kh * p.d, sub * 8, p.half, p.interleaved != 0,
+                          wcs + tok * p.cs_ld);
+            }
+            [[maybe_unused]] int byte = 127;
+            if constexpr (Q8) {
+                float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-            for (int o = group >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            byte = scale_byte(m);
-        }
-        if (!live) continue;
-        const long long dst_row = slot[tok];
-        const size_t o = ((size_t)dst_row * p.Hkv + h) * p.d + sub * 8;
-        if constexpr (Q8) {
-            const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);    // 2^-e, e <= 120
-            uint2 w;
-            __nv_fp8x2_storage_t c[4];
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+                for (int o = group >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                byte = scale_byte(m);
+            }
+            if (!live) continue;
+            const int h = is_v ? kh - p.Hkv : kh;
+            const size_t o = data_at[tok] + (h * p.d + sub * 8);
+            if constexpr (Q8) {
+                const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);    // 2^-e, e <= 120
+                uint2 w;
+                __nv_fp8x2_storage_t c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE,
-                                                __NV_E4M3);
-            w.x = (uint32_t)c[0] | ((uint32_t)c[1] << 16);
-            w.y = (uint32_t)c[2] | ((uint32_t)c[3] << 16);
-            *reinterpret_cast<uint2 *>((uint8_t *)(is_v ? p.c.v_pages : p.c.k_pages) + o) = w;
-            if (sub == 0) (is_v ? p.c.v_scale : p.c.k_scale)[scale_index(p.c, dst_row, p.Hkv, h)] = (uint8_t)byte;
-        } else {
-            store_n<8>((TO *)(is_v ? p.c.v_pages : p.c.k_pages) + o, x);
+                for (int i = 0; i < 4; ++i)
+                    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE,
+                                                    __NV_E4M3);
+                w.x = (uint32_t)c[0] | ((uint32_t)c[1] << 16);
+                w.y = (uint32_t)c[2] | ((uint32_t)c[3] << 16);
+                *reinterpret_cast<uint2 *>((uint8_t *)(is_v ? p.c.v_pages : p.c.k_pages) + o) = w;
+                if (sub == 0)
+                    (is_v ? p.c.v_scale : p.c.k_scale)[scale_at[tok] + ((size_t)h << p.c.page_shift)] = (uint8_t)byte;
+            } else {
+                store_n<8>((TO *)(is_v ? p.c.v_pages : p.c.k_pages) + o, x);
+            }
         }
     }
 }
 
 template <typename TI, typename TO, bool Q8>
 cudaError_t write_go(WriteParams p, cudaStream_t st) {
-    // two tokens a block once that still gives every SM its blocks
-    p.tokens = p.T >= 4096 ? 8 : (p.T >= 1024 ? 2 : 1);
+    // eight tokens a block once that still gives every SM several blocks: what a
+    // block does besides its rows (places, angles) is then an eighth (16959
+    // tokens of 8 heads, copied: four tokens 27.3 us, eight 25.5)
+    p.tokens = p.T >= 4096 ? kWriteTokens : 1;
+    p.cs_ld = (3 * p.half + 3) & ~3;               // whole 16-byte units for each token
+    p.group_shift = 0;                             // lanes of a row, rounded up to a power of two (<= 32)
+    while ((8 << p.group_shift) < p.d) ++p.group_shift;
+    p.dq = (kThreads >> p.group_shift) / (2 * p.Hkv);
+    p.dr = (kThreads >> p.group_shift) % (2 * p.Hkv);
     cache_write_kernel<TI, TO, Q8><<<(p.T + p.tokens - 1) / p.tokens, kThreads,
-                                     (size_t)p.tokens * p.half * sizeof(float2), st>>>(p);
+                                     (size_t)p.tokens * p.cs_ld * sizeof(float), st>>>(p);
     count_launch();
     return cudaGetLastError();
 }

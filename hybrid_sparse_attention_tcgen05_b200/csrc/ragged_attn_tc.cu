@@ -108,6 +108,7 @@ struct RaggedParams {
     PagedCache c;              // cu_rows, B; paged: kv_len, block_table, pages, scales
     int paged;
     int T, Hq, Hkv, G, tpt;    // tpt: tokens per 128-row tile (128 / G)
+    uint32_t g_inv;            // ceil(2^16 / G): row / G = row * g_inv >> 16 for rows below 128
     int box_rows;              // keys one TMA box brings
     int works, splits, chunk;  // work items planned for; pieces per item; key tiles per piece
     float scale_log2;
@@ -805,7 +806,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(w * 128);
         const float c2 = p.scale_log2;
         const float nan = __int_as_float(0x7fc00000);
-        const int row_tok = tw / p.G, row_head = tw - row_tok * p.G;
+        const int row_tok = (int)((uint32_t)tw * p.g_inv >> 16), row_head = tw - row_tok * p.G;
         Phase side_phase, o_phase;
         uint32_t steps_done = 0;       // steps of 64 keys so far: the buffer and the parities follow
         uint32_t k_tiles = 0;
@@ -921,15 +922,15 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(&bars->o_full[w]), o_phase.take(), p.wait_ns, abort));
             bool fin = ok;
             tc_fence_after();
-            // O of this thread's row: columns [16 c, 16 c + 16), zeros when there were no tiles
-            auto load_o = [&](int c, float (&o)[16]) {
-                uint32_t r[16];
+            // O of this thread's row: columns [32 c, 32 c + 32), zeros when there were no tiles
+            auto load_o = [&](int c, float (&o)[32]) {
+                uint32_t r[32];
                 if (nw > 0) {
-                    tmem_ld16(tO + 16 * c, r);
+                    tmem_ld32(tO + 32 * c, r);
                     tmem_wait_ld();
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = nw > 0 ? __uint_as_float(r[e]) : 0.f;
+                for (int e = 0; e < 32; ++e) o[e] = nw > 0 ? __uint_as_float(r[e]) : 0.f;
             };
             float *const side = reinterpret_cast<float *>(sq) + tw * 128;   // 64 KB: the Q tiles, no longer read
             float a0 = 1.f, a1 = 0.f;
@@ -938,13 +939,13 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 if (w == 1) {
                     bars->side[tw] = make_float2(fin ? m : nan, l);
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        float o[16];
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
                         load_o(c, o);
                         if (valid) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<float4 *>(side + (((4 * c + e) ^ (tw & 31)) << 2)) =
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<float4 *>(side + (((8 * c + e) ^ (tw & 31)) << 2)) =
                                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     }
@@ -987,56 +988,78 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 uint8_t *stage = so + (warp & 7) * 4096;
                 uint8_t *mine_at = stage + lane * 128;
                 const int rows32 = tw & ~31;
-                const int steps = partial ? 4 : 2;
-#pragma unroll 1
-                for (int c = 0; c < steps; ++c) {
-                    __syncwarp();                              // the step before has been read
-#pragma unroll 1
-                    for (int q = 0; q < (partial ? 2 : 4); ++q) {       // 16 columns each
-                        float o[16];
-                        const int col = partial ? 2 * c + q : 4 * c + q;
-                        load_o(col, o);
-                        if (join) {
+                // the rows that this lane stores, four apart: where they go, in rows of 128
+                // elements from p.out or p.part_o on (-1: nowhere)
+                int dst_row[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 y = *reinterpret_cast<const float4 *>(side + (((4 * col + e) ^ (tw & 31)) << 2));
-                                o[4 * e] = o[4 * e] * a0 + y.x * a1;
-                                o[4 * e + 1] = o[4 * e + 1] * a0 + y.y * a1;
-                                o[4 * e + 2] = o[4 * e + 2] * a0 + y.z * a1;
-                                o[4 * e + 3] = o[4 * e + 3] * a0 + y.w * a1;
-                            }
-                        } else {
+                for (int i = 0; i < 8; ++i) {
+                    const int tr = rows32 + 4 * i + (lane >> 3);
+                    const int t_tok = (int)((uint32_t)tr * p.g_inv >> 16), t = first + t_tok;
+                    dst_row[i] = tr < p.tpt * p.G && t < wk.ql ? t_tok * p.Hq + (tr - t_tok * p.G) : -1;
+                }
+                const size_t base = ((size_t)wk.q0 + first) * p.Hq + wk.g * p.G;
+                const int ch = lane & 7;
+                // 32 columns at a time: their place in the stage, and what joins them
+                auto columns = [&](int c, float (&o)[32]) {
+                    load_o(c, o);
+                    if (join) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= a0;
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 y = *reinterpret_cast<const float4 *>(side + (((8 * c + e) ^ (tw & 31)) << 2));
+                            o[4 * e] = o[4 * e] * a0 + y.x * a1;
+                            o[4 * e + 1] = o[4 * e + 1] * a0 + y.y * a1;
+                            o[4 * e + 2] = o[4 * e + 2] * a0 + y.z * a1;
+                            o[4 * e + 3] = o[4 * e + 3] * a0 + y.w * a1;
                         }
-                        if (partial) {
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= a0;
+                    }
+                };
+                if (partial) {
+                    float *dst = p.part_o + ((size_t)wk.piece * p.T * p.Hq + base) * HD + 4 * ch;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        columns(c, o);
+                        __syncwarp();                          // the step before has been read
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4 *>(mine_at + ((e ^ (lane & 7)) << 4)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {          // four rows a store, eight lanes each
+                            const int r = 4 * i + (lane >> 3);
+                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+                            if (dst_row[i] >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)dst_row[i] * HD + 32 * c) = x;
+                        }
+                    }
+                } else {
+                    __nv_bfloat16 *dst = p.out + base * HD + 8 * ch;
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float o[32];
+                            columns(2 * c + q, o);
+                            if (q == 0) __syncwarp();
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<float4 *>(mine_at + (((4 * q + e) ^ (lane & 7)) << 4)) =
-                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<uint4 *>(mine_at + (((2 * q + e) ^ (lane & 7)) << 4)) =
+                                *reinterpret_cast<uint4 *>(mine_at + (((4 * q + e) ^ (lane & 7)) << 4)) =
                                     make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
                                                pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                         }
-                    }
-                    __syncwarp();
+                        __syncwarp();
 #pragma unroll
-                    for (int r0 = 0; r0 < 32; r0 += 4) {       // four rows a store, eight lanes each
-                        const int r = r0 + (lane >> 3), ch = lane & 7;
-                        const int tr = rows32 + r, t_tok = tr / p.G, t = first + t_tok;
-                        if (tr < p.tpt * p.G && t < wk.ql) {
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3);
                             const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-                            const size_t at = (size_t)(wk.q0 + t) * p.Hq + wk.g * p.G + (tr - t_tok * p.G);
-                            if (partial)
-                                *reinterpret_cast<uint4 *>(p.part_o + ((size_t)wk.piece * p.T * p.Hq + at) * HD + 32 * c + 4 * ch) = x;
-                            else
-                                *reinterpret_cast<uint4 *>(p.out + at * HD + 64 * c + 8 * ch) = x;
+                            if (dst_row[i] >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)dst_row[i] * HD + 64 * c) = x;
                         }
                     }
                 }
+                __syncwarp();
             }
             if (w == 0 && join) {
                 fence_proxy_async_smem();
@@ -1277,6 +1300,7 @@ cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *
     p.c = a.cache;
     p.paged = a.paged;
     p.T = a.T; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.tpt = 128 / p.G;
+    p.g_inv = (65536u + p.G - 1) / p.G;
     const bool f8 = a.paged && a.cache.dtype == HS_E4M3;
     const int page = a.paged ? 1 << a.cache.page_shift : 0;
     p.box_rows = a.paged ? std::min(page, BN) : BN;
