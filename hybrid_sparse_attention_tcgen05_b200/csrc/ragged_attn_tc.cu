@@ -1185,7 +1185,7 @@ constexpr int kSms = 148;
 constexpr int kMaxSplits = 64;
 constexpr int kFewRows = 16;               // rows (new tokens x group) a sequence up to which the warp-MMA kernel runs
 constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an SM holds (bf16, 8-bit caches)
-constexpr int kFewRowsFixed = 8;           // what a piece costs besides its keys, in 16-key blocks
+constexpr int kFewRowsFixed = 16;          // what a piece costs besides its keys, in 16-key blocks
 constexpr int kFewRowsMinChunk = 4;        // fewest 16-key blocks in a piece (one for each warp)
 constexpr size_t kMaxPartRows = 180000;    // rows of partial results: 520 bytes each
 

@@ -79,6 +79,11 @@ def _dense(t: Optional[torch.Tensor], what: str, dtype=None, shape=None) -> None
         raise ValueError(f"{what} must be contiguous")
 
 
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _call(dev: int, fn, what: str, *args) -> None:
     """The library call on the tensors' device and that device's current stream."""
     if dev != _current_device():
@@ -170,24 +175,27 @@ def rope(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, k:
     if positions.dtype != torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
         raise TypeError("positions must be a contiguous int32 vector, one per row")
     if out is None:
-        out = q.new_empty((T, Hq, d))
+        out, ld_o = _like(q), Hq * d
+    else:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must be like q")
+        ld_o = _rows(out, "out")[3]
     Hkv, ld_k, ld_ok = 0, 0, 0
     if k is not None:
         Tk, Hkv, dk, ld_k = _rows(k, "k")
         if Tk != T or dk != d or k.dtype != q.dtype:
             raise ValueError("q and k disagree on rows, head dim or dtype")
         if out_k is None:
-            out_k = k.new_empty((T, Hkv, d))
-        if out_k.shape != k.shape or out_k.dtype != k.dtype:
-            raise ValueError("out_k must be like k")
-        ld_ok = _rows(out_k, "out_k")[3]
+            out_k, ld_ok = _like(k), Hkv * d
+        else:
+            if out_k.shape != k.shape or out_k.dtype != k.dtype:
+                raise ValueError("out_k must be like k")
+            ld_ok = _rows(out_k, "out_k")[3]
     elif out_k is not None:
         raise ValueError("out_k without k")
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must be like q")
     flags = (_lib.HS_ROPE_INTERLEAVED if interleaved else 0) | (_lib.HS_ROPE_INVERSE if inverse else 0)
     _call(dev, _lib.lib().hysparse_rope, "hysparse_rope", T, Hq, Hkv, d, _code(q.dtype), _p(q), ld_q, _p(k), ld_k,
-          _p(positions), _p(inv_freq), rot, flags, float(factor), _p(out), _rows(out, "out")[3], _p(out_k), ld_ok)
+          _p(positions), _p(inv_freq), rot, flags, float(factor), _p(out), ld_o, _p(out_k), ld_ok)
     return out if k is None else (out, out_k)
 
 
@@ -287,7 +295,7 @@ def _attn_buffers(q: torch.Tensor, Hkv: int, B: int, max_q: int, max_len: int, o
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
     if out is None:
-        out = q.new_empty((T, Hq, d))
+        out = _like(q)
     else:
         _dense(out, "out", q.dtype, (T, Hq, d))
     if lse is None:
