@@ -137,19 +137,50 @@ __device__ __forceinline__ void seq_bounds(const RaggedParams &p, int b, int &q0
     if (p.paged) kvl = min(max(__ldg(p.c.kv_len + b), 0), p.c.max_pages << p.c.page_shift);
 }
 
+// What the warp that finds items keeps from one to the next, so that the
+// batch is read once.  Up to 32 sequences: lane b holds sequence b.  More:
+// lane i holds how many row groups the sequences [i * per, (i + 1) * per)
+// have, and all up to them.
+struct Batch {
+    int q0 = 0, ql = 0, kvl = 0;
+    int sum = 0, upto = 0, per = 0;
+};
+
+__device__ __forceinline__ Batch read_batch(const RaggedParams &p) {
+    const int lane = threadIdx.x & 31, B = p.c.B, qt = 2 * p.tpt;
+    Batch t;
+    if (B <= 32) {
+        if (lane < B) seq_bounds(p, lane, t.q0, t.ql, t.kvl);
+        return t;
+    }
+    t.per = (B + 31) / 32;
+    const int first = min(lane * t.per, B), last = min(first + t.per, B);
+#pragma unroll 4
+    for (int i = first; i < last; ++i) {
+        int q0, ql, kvl;
+        seq_bounds(p, i, q0, ql, kvl);
+        t.sum += (ql + qt - 1) / qt;
+    }
+    t.upto = t.sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, t.upto, o);
+        if (lane >= o) t.upto += y;
+    }
+    return t;
+}
+
 // Which sequence and rows work item `idx` is (one warp).  Up to 32 sequences:
 // items in descending order of their keys, so that the longest start first.
 // More: in order, each sequence's last rows first.
-__device__ __forceinline__ bool find_rows(const RaggedParams &p, int idx, Work *w) {
+__device__ __forceinline__ bool find_rows(const RaggedParams &p, const Batch &bt, int idx, Work *w) {
     const int lane = threadIdx.x & 31;
     const int qt = 2 * p.tpt;
     const int B = p.c.B;
     int b = -1, t = 0;
     if (B <= 32) {
-        int q0, ql = 0, kvl = 0;
-        if (lane < B) seq_bounds(p, lane, q0, ql, kvl);
-        const int nt = (ql + qt - 1) / qt;
-        const int base = max(kvl - ql, 0) / qt;
+        const int nt = (bt.ql + qt - 1) / qt;
+        const int base = max(bt.kvl - bt.ql, 0) / qt;
         const int total = __reduce_add_sync(0xffffffffu, nt);
         if (idx == 0 && lane == 0 && total > p.works) report(p.status, HS_ERR_INVALID_ARG);
         if (idx >= total) return false;
@@ -163,43 +194,42 @@ __device__ __forceinline__ bool find_rows(const RaggedParams &p, int idx, Work *
         const unsigned there = __ballot_sync(0xffffffffu, lo >= base && lo < base + nt);
         b = __fns(there, 0, idx - past + 1);
         t = lo - __shfl_sync(0xffffffffu, base, b);
+        w->q0 = __shfl_sync(0xffffffffu, bt.q0, b);
+        w->ql = __shfl_sync(0xffffffffu, bt.ql, b);
+        w->kvl = __shfl_sync(0xffffffffu, bt.kvl, b);
     } else {
-        const int per = (B + 31) / 32, first = lane * per, last = min(first + per, B);
-        int sum = 0;
-        for (int i = first; i < last; ++i) {
-            int q0, ql, kvl;
-            seq_bounds(p, i, q0, ql, kvl);
-            sum += (ql + qt - 1) / qt;
-        }
-        int upto = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const int total = __shfl_sync(0xffffffffu, upto, 31);
+        const int total = __shfl_sync(0xffffffffu, bt.upto, 31);
         if (idx == 0 && lane == 0 && total > p.works) report(p.status, HS_ERR_INVALID_ARG);
         if (idx >= total) return false;
-        const int owner = __ffs(__ballot_sync(0xffffffffu, upto > idx)) - 1;
-        if (lane == owner) {
-            int left = idx - (upto - sum);
-            for (int i = first; i < last; ++i) {
-                int q0, ql, kvl;
-                seq_bounds(p, i, q0, ql, kvl);
-                const int nt = (ql + qt - 1) / qt;
-                if (left < nt) {
-                    b = i;
-                    t = nt - 1 - left;
-                    break;
-                }
-                left -= nt;
+        // the lane whose sequences the item is among, then those, 32 at a time
+        const int owner = __ffs(__ballot_sync(0xffffffffu, bt.upto > idx)) - 1;
+        int left = idx - __shfl_sync(0xffffffffu, bt.upto - bt.sum, owner);
+        const int first = owner * bt.per, last = min(first + bt.per, B);
+        for (int i0 = first; i0 < last; i0 += 32) {
+            int q0 = 0, ql = 0, kvl = 0;
+            if (i0 + lane < last) seq_bounds(p, i0 + lane, q0, ql, kvl);
+            const int nt = (ql + qt - 1) / qt;
+            int upto = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
             }
+            const unsigned past = __ballot_sync(0xffffffffu, upto > left);
+            if (past != 0) {
+                const int src = __ffs(past) - 1;
+                b = i0 + src;
+                t = __shfl_sync(0xffffffffu, upto, src) - 1 - left;      // last rows first
+                w->q0 = __shfl_sync(0xffffffffu, q0, src);
+                w->ql = __shfl_sync(0xffffffffu, ql, src);
+                w->kvl = __shfl_sync(0xffffffffu, kvl, src);
+                break;
+            }
+            left -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        b = __shfl_sync(0xffffffffu, b, owner);
-        t = __shfl_sync(0xffffffffu, t, owner);
+        if (b < 0) return false;       // (the batch changed under the call)
     }
     w->b = b;
-    seq_bounds(p, b, w->q0, w->ql, w->kvl);
     if (lane == 0 && (__ldg(p.c.cu_rows + b + 1) > p.T || __ldg(p.c.cu_rows + b) < 0 ||
                       (p.paged && __ldg(p.c.kv_len + b) != w->kvl)))
         report(p.status, HS_ERR_INVALID_ARG);
@@ -212,14 +242,14 @@ __device__ __forceinline__ int key_tiles(int last_pos) { return last_pos < 0 ? 0
 
 // The i-th item of this CTA (one warp): items are numbered work, piece, KV
 // head (fastest) and dealt to the CTAs forth and back.
-__device__ __forceinline__ Work find_work(const RaggedParams &p, int i) {
+__device__ __forceinline__ Work find_work(const RaggedParams &p, const Batch &bt, int i) {
     Work w{};
     const long long id = (long long)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (id >= (long long)p.works * p.splits * p.Hkv) return w;
     const int item = (int)(id / p.Hkv);
     w.g = (int)(id - (long long)item * p.Hkv);
     w.piece = item % p.splits;
-    if (!find_rows(p, item / p.splits, &w)) return w;
+    if (!find_rows(p, bt, item / p.splits, &w)) return w;
     const int nq = min(2 * p.tpt, w.ql - w.t0);
     const int nk = key_tiles(w.off + w.t0 + nq - 1);
     const int nk0 = key_tiles(w.off + w.t0 + min(p.tpt, nq) - 1);
@@ -343,8 +373,11 @@ __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t leader) {
         : "memory");
 }
 
-// mbar_wait whose first poll does not suspend the thread: with a limit of 0
-// it gives up whenever the phase is not complete yet.
+// mbar_wait for warps that share their scheduler with others' arithmetic:
+// the first poll does not suspend the thread (with a limit of 0 the wait
+// gives up whenever the phase is not complete yet), the others suspend it
+// for up to kSuspendNs, so that waiting takes no issue slots.
+constexpr uint32_t kSuspendNs = 20000;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort) {
     uint32_t there;
     asm volatile(
@@ -357,7 +390,21 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint64_t
         *abort = 1;
         return false;
     }
-    return mbar_wait(bar, parity, limit_ns, abort);
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(there)
+            : "r"(bar), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (there) return true;
+        if (*abort) return false;
+        if (globaltimer() - t0 > limit_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
 }
 
 // A count of uses whose parity a barrier's waits follow.
@@ -473,8 +520,9 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         regs_release<R::ctl>();
         if (warp == 11) {
             // ------------------------------------------------ items
+            const Batch bt = read_batch(p);
             for (int i = 0;; ++i) {
-                const Work w = find_work(p, i);
+                const Work w = find_work(p, bt, i);
                 const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->work_empty[i & 1]), ((i >> 1) & 1) ^ 1,
                                                                   p.wait_ns, abort));
                 if (!ok) break;
@@ -1073,8 +1121,9 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         // a wait gave up: the rows of the items that this CTA did not get to
         // are marked like those of the one it was at
         if (*abort && (warp & 3) == 0) {
+            const Batch bt = read_batch(p);
             for (int i = work_i;; ++i) {
-                const Work x = find_work(p, i);
+                const Work x = find_work(p, bt, i);
                 if (!x.go) break;
                 if (x.solo && w == 1) continue;
                 for (int r = lane; r < p.tpt * p.G; r += 32) {

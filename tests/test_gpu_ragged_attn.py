@@ -94,6 +94,25 @@ def test_packed_many_sequences():
         ref.check_attend(f"seq {b}", out[part], lse[:, part], ref.attend(q[part], k[part], v[part], SCALE))
 
 
+@pytest.mark.parametrize("B", [33, 64, 1100, 2500])
+def test_packed_more_sequences_than_lanes(B):
+    """Batches whose items are found in two steps, with runs of empty sequences, and several items in
+    some sequences; rows of a few sequences against the definition, all of them finite."""
+    gen = torch.Generator().manual_seed(B)
+    lens = [0 if r < 3 else r for r in torch.randint(0, 12, (B,), generator=gen).tolist()]
+    lens[B // 2:B // 2 + 40] = [0] * min(40, B - B // 2)
+    lens[-1], lens[B // 3], lens[5] = 200, 131, 64
+    hq, hkv, T = 4, 1, sum(lens)
+    q, k, v = (torch.randn(T, h, 128, generator=gen).to(BF) for h in (hq, hkv, hkv))
+    cu = ref.cu_of(lens)
+    out = torch.full((T, hq, 128), math.nan, dtype=BF, device=DEV)
+    _, lse = hs.packed_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), max_len=200, out=out)
+    assert bool(torch.isfinite(out.float()).all())
+    for b in [0, 1, 5, 31, 32, B // 3, B // 2 - 1, min(B // 2 + 40, B - 1), B - 2, B - 1]:
+        part = slice(int(cu[b]), int(cu[b]) + lens[b])
+        ref.check_attend(f"seq {b}", out[part], lse[:, part], ref.attend(q[part], k[part], v[part], SCALE))
+
+
 def test_packed_equals_full_layer():
     """Equal prompts: the full layer of the hybrid block, prompt by prompt, to rounding (both round P
     and the output to bf16: twice check_attend's terms)."""
