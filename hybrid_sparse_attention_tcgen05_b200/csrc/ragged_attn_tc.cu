@@ -37,7 +37,6 @@
 // clock (64-key Q K^T: 48 KB in 256 clocks of products).
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -414,7 +413,7 @@ struct Phase {
     __device__ __forceinline__ uint32_t take_free() { return (n++ & 1) ^ 1; }   // of the phase before it (free at the start)
 };
 
-// 2^x for two x in about [-126, 8]: 2^n by the exponent field, n = rint(x),
+// 2^x for two x up to 8 (2^-126 below -126): 2^n by the exponent field, n = rint(x),
 // times a polynomial for the rest in [-0.5, 0.5] (degree 4, minimax in
 // relative error by the exchange algorithm: 2.6e-6, 1/1500 of a bf16
 // rounding, and 1.4e-8 on average, so sums of many keep fp32's accuracy).  It
@@ -436,8 +435,8 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
                        __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
 }
 
-// Of every 8 pairs of probabilities in a tile without masked keys, how many
-// come from exp2_fma.
+// Of every 8 pairs of probabilities, how many come from exp2_fma (8192-token
+// prompt, 64/4 heads: none 1008 us, two 975, four 1020).
 constexpr int kFmaPairs = 2;
 
 template <bool F8>
@@ -894,16 +893,18 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const bool lost = p.paged && bars->bad_any[bad] != 0;
                 const bool masked = lost || key0 + 63 > pos_first;
                 if (masked) {
-                    // one bit a key: up to the row's own position, and not on a lost page
-                    const int seen = pos - key0 + 1;
+                    // keys up to the row's own position, and not on a lost page
+                    const int seen = pos - key0;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int k = min(max(seen - 32 * q, 0), 32);
-                        uint32_t bits = k == 32 ? 0xffffffffu : (1u << k) - 1u;
-                        if (lost) bits &= ~bars->bad[bad][2 * buf + q];
+                    for (int c = 0; c < 64; ++c) s[c] = c <= seen ? s[c] : -INFINITY;
+                    if (lost) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((bits >> c) & 1u)) s[32 * q + c] = -INFINITY;
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t bits = bars->bad[bad][2 * buf + q];
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if ((bits >> c) & 1u) s[32 * q + c] = -INFINITY;
+                        }
                     }
                 }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
@@ -938,28 +939,25 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     }
                     m = m_new;
                 }
-                const float mref = m == -INFINITY ? 0.f : m;   // masked keys (-inf) give 2^-inf = 0
+                // masked keys (-inf) give 0, or 2^-126 by exp2_fma, which beside a seen
+                // key's is nothing; a row that has seen none is set right at the end
+                const float mref = m == -INFINITY ? 0.f : m;
                 const float2 c2v = make_float2(c2, c2), mv = make_float2(-mref, -mref);
                 float2 ps01 = make_float2(0.f, 0.f), ps23 = make_float2(0.f, 0.f);
-                auto probabilities = [&](auto fma_pairs) {
 #pragma unroll
-                    for (int ch = 0; ch < 2; ++ch) {
-                        uint32_t pk[16];
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int c = ch * 32 + 2 * e;
-                            const float2 t = ffma2(make_float2(s[c], s[c + 1]), c2v, mv);
-                            const float2 ab = (e & 7) < decltype(fma_pairs)::value ? exp2_fma(t)
-                                                                                   : make_float2(ex2(t.x), ex2(t.y));
-                            if (e & 1) ps23 = fadd2(ps23, ab); else ps01 = fadd2(ps01, ab);
-                            // P is rounded to bf16, the type of V: one MMA takes one type
-                            pk[e] = pack_bf16(ab.x, ab.y);
-                        }
-                        tmem_st16(tS + buf * 64 + 16 * ch, pk);
+                    for (int e = 0; e < 16; ++e) {
+                        const int c = ch * 32 + 2 * e;
+                        const float2 t = ffma2(make_float2(s[c], s[c + 1]), c2v, mv);
+                        const float2 ab = (e & 7) < kFmaPairs ? exp2_fma(t) : make_float2(ex2(t.x), ex2(t.y));
+                        if (e & 1) ps23 = fadd2(ps23, ab); else ps01 = fadd2(ps01, ab);
+                        // P is rounded to bf16, the type of V: one MMA takes one type
+                        pk[e] = pack_bf16(ab.x, ab.y);
                     }
-                };
-                if (masked) probabilities(std::integral_constant<int, 0>());   // exp2_fma would not give 0 for a masked key
-                else probabilities(std::integral_constant<int, kFmaPairs>());
+                    tmem_st16(tS + buf * 64 + 16 * ch, pk);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars->p_full[w][buf]));
@@ -969,6 +967,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             if (nw > 0)
                 ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(&bars->o_full[w]), o_phase.take(), p.wait_ns, abort));
             bool fin = ok;
+            if (m == -INFINITY) l = 0.f;               // nothing seen
             tc_fence_after();
             // O of this thread's row: columns [32 c, 32 c + 32), zeros when there were no tiles
             auto load_o = [&](int c, float (&o)[32]) {
@@ -1036,19 +1035,14 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 uint8_t *stage = so + (warp & 7) * 4096;
                 uint8_t *mine_at = stage + lane * 128;
                 const int rows32 = tw & ~31;
-                // the rows that this lane stores, four apart: where they go, in rows of 128
-                // elements from p.out or p.part_o on (-1: nowhere)
-                int dst_row[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int tr = rows32 + 4 * i + (lane >> 3);
-                    const int t_tok = (int)((uint32_t)tr * p.g_inv >> 16), t = first + t_tok;
-                    dst_row[i] = tr < p.tpt * p.G && t < wk.ql ? t_tok * p.Hq + (tr - t_tok * p.G) : -1;
-                }
-                const size_t base = ((size_t)wk.q0 + first) * p.Hq + wk.g * p.G;
-                const int ch = lane & 7;
-                // 32 columns at a time: their place in the stage, and what joins them
-                auto columns = [&](int c, float (&o)[32]) {
+                // Four rows a store, eight lanes each.
+                const int r_mine = lane >> 3, ch = lane & 7;
+                const int el = partial ? 4 : 2;                        // bytes of a result
+                uint8_t *const base = (partial ? (uint8_t *)(p.part_o + (size_t)wk.piece * p.T * p.Hq * HD) : (uint8_t *)p.out) +
+                                      (((size_t)wk.q0 + first) * p.Hq + wk.g * p.G) * (HD * el) + 16 * ch;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {                          // 32 columns
+                    float o[32];
                     load_o(c, o);
                     if (join) {
 #pragma unroll
@@ -1063,51 +1057,36 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= a0;
                     }
-                };
-                if (partial) {
-                    float *dst = p.part_o + ((size_t)wk.piece * p.T * p.Hq + base) * HD + 4 * ch;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float o[32];
-                        columns(c, o);
-                        __syncwarp();                          // the step before has been read
+                    if (partial) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             *reinterpret_cast<float4 *>(mine_at + ((e ^ (lane & 7)) << 4)) =
                                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        __syncwarp();
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {          // four rows a store, eight lanes each
-                            const int r = 4 * i + (lane >> 3);
-                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-                            if (dst_row[i] >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)dst_row[i] * HD + 32 * c) = x;
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4 *>(mine_at + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
+                                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                     }
-                } else {
-                    __nv_bfloat16 *dst = p.out + base * HD + 8 * ch;
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
+                    if (!partial && (c & 1) == 0) continue;            // half of the stage's 128 bytes
+                    __syncwarp();
+                    uint8_t *const to = base + (partial ? c : c >> 1) * 128;
+                    uint4 x[8];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float o[32];
-                            columns(2 * c + q, o);
-                            if (q == 0) __syncwarp();
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4 *>(mine_at + (((4 * q + e) ^ (lane & 7)) << 4)) =
-                                    make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                               pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3);
-                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-                            if (dst_row[i] >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)dst_row[i] * HD + 64 * c) = x;
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + r_mine;
+                        x[i] = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int tr = rows32 + 4 * i + r_mine;
+                        const int t_tok = (int)((uint32_t)tr * p.g_inv >> 16);
+                        if (tr < p.tpt * p.G && first + t_tok < wk.ql)
+                            *reinterpret_cast<uint4 *>(to + (size_t)(t_tok * p.Hq + (tr - t_tok * p.G)) * (HD * el)) = x[i];
+                    }
+                    __syncwarp();                                      // read before it is written again
                 }
-                __syncwarp();
             }
             if (w == 0 && join) {
                 fence_proxy_async_smem();
