@@ -1143,17 +1143,29 @@ __global__ void __launch_bounds__(256) ragged_combine(const RaggedParams p) {
     m = warp_max(m);
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 ml = p.part_ml[s * rows + r];
-        if (ml.x == -INFINITY) continue;                    // nothing seen in this piece
-        const float a = exp2f(ml.x - m);                    // NaN (a piece that gave up) carries through
-        l += a * ml.y;
-        const float4 o = *reinterpret_cast<const float4 *>(p.part_o + (s * rows + r) * HD + lane * 4);
-        acc.x += a * o.x;
-        acc.y += a * o.y;
-        acc.z += a * o.z;
-        acc.w += a * o.w;
+    for (int s0 = 0; s0 < p.splits; s0 += 32) {
+        // one piece a lane: its weight, 0 when it saw nothing (its O was not
+        // written then); NaN of a piece that gave up carries through
+        float a = 0.f;
+        if (s0 + lane < p.splits) {
+            const float2 ml = p.part_ml[(s0 + lane) * rows + r];
+            a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+            l += ml.x == -INFINITY ? 0.f : a * ml.y;
+        }
+        const int n = min(32, p.splits - s0);
+        const float *src = p.part_o + (s0 * rows + r) * HD + lane * 4;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            const float f = __shfl_sync(0xffffffffu, a, j);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f != 0.f) o = *reinterpret_cast<const float4 *>(src + j * rows * HD);
+            acc.x += f * o.x;
+            acc.y += f * o.y;
+            acc.z += f * o.z;
+            acc.w += f * o.w;
+        }
     }
+    l = warp_sum(l);
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint2 w;
     w.x = pack_bf16(acc.x * inv, acc.y * inv);
@@ -1211,7 +1223,12 @@ cudaError_t prepare() {
 
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 64;
-constexpr int kFewRows = 16;               // rows (new tokens x group) a sequence up to which the warp-MMA kernel runs
+// Rows (new tokens x group) a sequence up to which the warp-MMA kernel runs.
+// Measured with 32 / 8 heads, 16 caches of 8192, 64 of 2048 (us; 8, 16, 32, 64
+// rows): bf16 91, 91, 118, 233 against 120 of the tcgen05 kernel, and 87, 91,
+// 153, 222 against 138; 8-bit 62, 81, 144, 276 against 226, and 79, 110, 161,
+// 246 against 247.
+constexpr int kFewRows16 = 16, kFewRows8 = 32;
 constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an SM holds (bf16, 8-bit caches)
 constexpr int kFewRowsFixed = 16;          // what a piece costs besides its keys, in 16-key blocks
 constexpr int kFewRowsMinChunk = 4;        // fewest 16-key blocks in a piece (one for each warp)
@@ -1267,7 +1284,7 @@ RaggedPlan ragged_plan(const RaggedCall &a) {
     const size_t rows = (size_t)a.T * a.Hq;
     const int G = a.Hq / a.Hkv;
     const long long row_most = (long long)std::max(1, std::min(a.max_q, a.T)) * G;   // rows of a sequence, at most
-    if (a.paged && row_most <= kFewRows) {
+    if (a.paged && row_most <= (a.cache.dtype == HS_E4M3 ? kFewRows8 : kFewRows16)) {
         // few rows a sequence: 8- or 16-row tiles on the warp MMAs, pieces of 16-key blocks
         pl.few_rows = true;
         pl.tile_rows = row_most <= 8 ? 8 : 16;
