@@ -46,6 +46,9 @@ namespace {
 
 constexpr int kWarps = 4;          // per CTA
 constexpr int kBlock = 16;         // keys a warp takes at a time
+// Reference of a row that has seen no key: finite, so that differences with
+// it need no special case, and below every score but the last float's.
+constexpr float kNone = -3.4e38f;
 
 template <bool F8> struct Cfg {
     static constexpr int row = F8 ? 128 : 256;                     // bytes of a K or V row
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
             for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            mx[t][e] = my[t][e] = -INFINITY;
+            mx[t][e] = my[t][e] = kNone;
             l[t][e] = 0.f;
         }
     }
@@ -396,8 +399,8 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
                     }
                     if (!F8) tx = ty;
                     const float ny = fmaxf(my[t][e], ty), nx = fmaxf(mx[t][e], tx);
-                    const float cy = ny == -INFINITY ? 1.f : ex2(my[t][e] - ny);
-                    l[t][e] *= nx == -INFINITY ? 1.f : ex2(mx[t][e] - nx);
+                    const float cy = ex2(my[t][e] - ny);
+                    l[t][e] *= ex2(mx[t][e] - nx);
                     my[t][e] = ny;
                     mx[t][e] = nx;
 #pragma unroll
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
             float pr[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float ry = my[t][e] == -INFINITY ? 0.f : my[t][e], rx = mx[t][e] == -INFINITY ? 0.f : mx[t][e];
+                const float ry = my[t][e], rx = mx[t][e];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     pr[2 * k + e] = ex2(y[t][2 * k + e] - ry);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
     // eight threads a row, 16 dimensions each
     const int r = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * 16;
     if (r >= nrows) return;
-    float Mx = -INFINITY, My = -INFINITY, L = 0.f;
+    float Mx = kNone, My = kNone, L = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         Mx = fmaxf(Mx, stat[w * ROWS + r]);
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         const float ax = stat[w * ROWS + r], ay = stat[(kWarps + w) * ROWS + r];
-        if (ax == -INFINITY) continue;                           // saw nothing
+        if (ax == kNone) continue;                               // saw nothing
         L += stat[(2 * kWarps + w) * ROWS + r] * exp2f(ax - Mx);
         const float f = exp2f(ay - My);
         const float *src = reinterpret_cast<const float *>(smem) + (w * ROWS + r) * 128;
@@ -519,10 +522,10 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
     const int gr = ROWS * tile + r, tok = gr / p.G, h = g * p.G + gr % p.G;
     const size_t row = (size_t)q0 + tok;
     // O is in units of 2^My, the sum in units of 2^Mx
-    const float unit = Mx == -INFINITY ? 0.f : exp2f(My - Mx);
+    const float unit = Mx == kNone ? 0.f : exp2f(My - Mx);
     if (partial) {
         const size_t pr = ((size_t)piece * p.T + row) * p.Hq + h;
-        if (d0 == 0) p.part_ml[pr] = make_float2(Mx, L);
+        if (d0 == 0) p.part_ml[pr] = make_float2(Mx == kNone ? -INFINITY : Mx, L);
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
             *reinterpret_cast<float4 *>(p.part_o + pr * 128 + d0 + k) =
