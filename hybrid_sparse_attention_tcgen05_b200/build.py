@@ -4,7 +4,9 @@
 
 Each ``csrc/*.cu`` compiles to ``_build/<name>.o`` (in parallel, only when
 stale), then everything links into ``hybrid_sparse_attention_tcgen05_b200/
-libhysparse.so`` with the CUDA runtime linked statically.
+libhysparse.so`` with the CUDA runtime linked statically.  ``csrc/binding.cpp``
+becomes ``_binding.so``, the native half of ragged.py, against the torch that
+is installed.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhysparse.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -51,6 +54,36 @@ def _compile(src: str, obj: str, ptxas_verbose: bool) -> str:
     return res.stderr
 
 
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           "-isystem", f"{t}/include", "-isystem", f"{t}/include/torch/csrc/api/include",
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           f"-L{t}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for binding.cpp:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+
+
+def _binding_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    import torch
+
+    newest = max(os.path.getmtime(f) for f in (os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "hysparse.h"),
+                                               os.path.join(os.path.dirname(torch.__file__), "version.py")))
+    return os.path.getmtime(BINDING) < newest
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -63,6 +96,8 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
         if force or ptxas_verbose or not os.path.exists(obj) or \
                 os.path.getmtime(obj) < max(os.path.getmtime(src), dep_t):
             jobs.append((src, obj))
+    if force or _binding_stale():
+        _build_binding()
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
             futs = {ex.submit(_compile, s, o, ptxas_verbose): s for s, o in jobs}
