@@ -300,12 +300,16 @@ struct RingPos {
     }
 };
 
-// Two 8-bit floats (in the high bytes of both 16-bit halves of x) to a bf16
-// pair scaled by 2^-120: the sign stays, the code's four exponent bits go to
-// the low end of the bf16 exponent, whose bias is larger by 120; subnormal
-// codes become subnormal bf16 numbers.
-__device__ __forceinline__ uint32_t e4m3_to_bf16_tiny(uint32_t x) {
-    return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+// Two of the four 8-bit floats of w to a bf16 pair scaled by 2^-120: the sign
+// stays, the code's four exponent bits go to the low end of the bf16 exponent,
+// whose bias is larger by 120; subnormal codes become subnormal bf16 numbers.
+// The byte permutation puts each code's sign into all bits of the byte above
+// it, so that one shift and one mask are left (sel: 0x9180 for the lower two).
+template <int sel>
+__device__ __forceinline__ uint32_t e4m3_to_bf16_tiny(uint32_t w) {
+    uint32_t t;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w), "n"(sel));
+    return (t << 4) & 0x87f087f0u;
 }
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -770,13 +774,12 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             // ------------------------------------------------ 8-bit rows to bf16 tiles
             const int t = threadIdx.x - 384;
             const int c16 = t & 7, r0 = t >> 3;      // 16 codes of rows r0, r0 + 16, ...
-            // the two 16-byte chunks these codes become, of the row's 16 (8 a half);
-            // lanes of the second half store them in the other order, so that the
-            // eight lanes of a store phase touch all banks
-            const bool second = c16 >= 4;
-            const int ch0 = ((2 * c16) & 7) + (second ? 1 : 0), ch1 = ((2 * c16) & 7) + (second ? 0 : 1);
+            // read and stored as two halves of 8 codes, in an order that lets the
+            // lanes of each access touch all banks
+            const int first = (c16 >= 4) ^ (r0 & 1);
             const uint32_t row_at = (c16 >> 2) * HALF + r0 * 128;
-            const uint32_t at0 = row_at + ((ch0 ^ (r0 & 7)) << 4), at1 = row_at + ((ch1 ^ (r0 & 7)) << 4);
+            const uint32_t at0 = row_at + ((((2 * c16) & 7) + first) ^ (r0 & 7)) * 16;
+            const uint32_t at1 = row_at + ((((2 * c16) & 7) + 1 - first) ^ (r0 & 7)) * 16;
             RingPos st, kv;
             uint32_t tiles = 0;
             bool ok = true;
@@ -815,25 +818,25 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     // rows that are not there keep finite leftovers: their probabilities are exactly 0
 #pragma unroll 4
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(src + i * 2048);
+                        const uint2 u = *reinterpret_cast<const uint2 *>(src + i * 2048 + first * 8);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src + i * 2048 + 8 - first * 8);
                         const uint32_t sb = bars->scale[buf][r0 + 16 * i];
+                        const uint32_t w[4] = {u.x, u.y, v.x, v.y};
+                        uint32_t o[8];
                         // 2^(120 + byte - 127) as a bf16 pair, up to 2^127
                         uint32_t f = min(sb, 134u) * 0x00800080u + 0x3c003c00u;
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t o[8];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny(__byte_perm(w[q], 0, 0x1404)), f);
-                            o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny(__byte_perm(w[q], 0, 0x3424)), f);
+                            o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny<0x9180>(w[q]), f);
+                            o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny<0xb3a2>(w[q]), f);
                         }
                         if (sb > 134u) {       // the rest of a scale above 2^7
                             f = (sb - 134u) * 0x00800080u + 0x3f803f80u;
 #pragma unroll
                             for (int q = 0; q < 8; ++q) o[q] = bf16x2_mul(o[q], f);
                         }
-                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                        *reinterpret_cast<uint4 *>(dst + at0 + i * 2048) = second ? hi : lo;
-                        *reinterpret_cast<uint4 *>(dst + at1 + i * 2048) = second ? lo : hi;
+                        *reinterpret_cast<uint4 *>(dst + at0 + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(dst + at1 + i * 2048) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(&bars->kv_full[kv.slot]));
