@@ -251,12 +251,19 @@ __device__ __forceinline__ void turn8(float (&x)[8], const float (&y)[8], const 
     }
 }
 
+// The larger of two; NaN when one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The exponent byte (e + 127) of the smallest power of two 2^e with
 // amax <= 448 * 2^e, 448 being the largest 8-bit float; 2^0 for a row of
-// zeros.  448 = 1.75 * 2^8, so e follows from amax's own exponent and from
+// zeros, 255 when amax is NaN.  448 = 1.75 * 2^8, so e follows from amax's own exponent and from
 // whether its mantissa is above 1.75.
 __device__ __forceinline__ int scale_byte(float amax) {
-    if (!(amax > 0.f)) return 127;
+    if (!(amax > 0.f)) return amax == amax ? 127 : 255;
     const uint32_t u = __float_as_uint(amax);
     const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     return e < 1 ? 1 : e;
@@ -368,15 +375,16 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const WritePar
             if constexpr (Q8) {
                 float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-                for (int o = group >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+                for (int o = group >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 byte = scale_byte(m);
             }
             if (!live) continue;
             const int h = is_v ? kh - p.Hkv : kh;
             const size_t o = data_at[tok] + (h * p.d + sub * 8);
             if constexpr (Q8) {
-                const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);    // 2^-e, e <= 120
+                // 2^-e, e <= 120; NaN, which makes every code NaN, for a row that holds one
+                const float inv = __uint_as_float(byte == 255 ? 0x7fc00000u : (uint32_t)(254 - byte) << 23);
                 uint2 w;
                 __nv_fp8x2_storage_t c[4];
 #pragma unroll

@@ -83,6 +83,8 @@ int run_attn(const RaggedCall &a, void *ws, size_t ws_bytes, hs_stream_t stream)
     if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4) || !row_stride_ok(a.ld_q, a.Hq, 128, HS_BF16))
         return HS_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return HS_ERR_INVALID_ARG;
+    // other rows' work items still read these when the first results are written
+    if (a.out == a.q || a.out == a.k || a.out == a.v) return HS_ERR_INVALID_ARG;
     const RaggedPlan pl = ragged_plan(a);
     if (ws_bytes < pl.bytes) return HS_ERR_WORKSPACE;
     const cudaError_t e = ragged_attn_launch(a, pl, ws, wait_limit_ns(), (cudaStream_t)stream);

@@ -417,7 +417,14 @@ struct Phase {
     __device__ __forceinline__ uint32_t take_free() { return (n++ & 1) ^ 1; }   // of the phase before it (free at the start)
 };
 
-// 2^x for two x up to 8 (2^-126 below -126): 2^n by the exponent field, n = rint(x),
+// Largest of three; NaN when one of them is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^x for two x up to 8 (2^-126 below -126 and for NaN): 2^n by the exponent field, n = rint(x),
 // times a polynomial for the rest in [-0.5, 0.5] (degree 4, minimax in
 // relative error by the exchange algorithm: 2.6e-6, 1/1500 of a bf16
 // rounding, and 1.4e-8 on average, so sums of many keep fp32's accuracy).  It
@@ -830,8 +837,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                             o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny<0x9180>(w[q]), f);
                             o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny<0xb3a2>(w[q]), f);
                         }
-                        if (sb > 134u) {       // the rest of a scale above 2^7
-                            f = (sb - 134u) * 0x00800080u + 0x3f803f80u;
+                        if (sb > 134u) {       // the rest of a scale above 2^7, or a row of NaN
+                            f = sb == 255u ? 0x7fff7fffu : (sb - 134u) * 0x00800080u + 0x3f803f80u;
 #pragma unroll
                             for (int q = 0; q < 8; ++q) o[q] = bf16x2_mul(o[q], f);
                         }
@@ -912,12 +919,13 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int c = 4; c < 64; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
-                const float mx2 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+                for (int c = 4; c < 64; c += 2) m4[(c >> 1) & 3] = fmax3_nan(m4[(c >> 1) & 3], s[c], s[c + 1]);
+                const float mx2 = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * c2;
                 // the running maximum only moves when it grows by more than 8 (log2
                 // units); the final division uses the same reference
-                if (__any_sync(0xffffffffu, mx2 > m + 8.0f)) {
-                    const float m_new = fmaxf(m, mx2);
+                if (__any_sync(0xffffffffu, !(mx2 <= m + 8.0f))) {
+                    // (a score that is NaN or +inf makes the row NaN, here and for good)
+                    const float m_new = mx2 < INFINITY ? fmax3_nan(m, mx2, mx2) : nan;
                     if (u > 0) {
                         // The product of the step before has to be in O first.  (Its phase is
                         // the barrier's last or current one: the step before that is done,
@@ -1025,7 +1033,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 else {
                     if (p.splits > 1) p.part_ml[pr] = make_float2(0.f, -1.f);
                     // a bounded wait gave up: NaN in the row's lse, as in the full layer
-                    p.lse[(size_t)h * p.T + row] = !fin ? nan : (l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY);
+                    p.lse[(size_t)h * p.T + row] = !fin || l != l ? nan : (l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY);
                 }
             }
             if (mine && (partial ? n > 0 : wk.piece == 0)) {
@@ -1169,7 +1177,7 @@ __global__ void __launch_bounds__(256) ragged_combine(const RaggedParams p) {
         }
     }
     l = warp_sum(l);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? 1.f / l : (l != l ? l : 0.f);
     uint2 w;
     w.x = pack_bf16(acc.x * inv, acc.y * inv);
     w.y = pack_bf16(acc.z * inv, acc.w * inv);

@@ -506,8 +506,9 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         const float ax = stat[w * ROWS + r], ay = stat[(kWarps + w) * ROWS + r];
-        if (ax == kNone) continue;                               // saw nothing
-        L += stat[(2 * kWarps + w) * ROWS + r] * exp2f(ax - Mx);
+        const float lw = stat[(2 * kWarps + w) * ROWS + r];
+        if (lw == 0.f) continue;                                 // saw nothing
+        L += lw * exp2f(ax - Mx);
         const float f = exp2f(ay - My);
         const float *src = reinterpret_cast<const float *>(smem) + (w * ROWS + r) * 128;
 #pragma unroll
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
     const float unit = Mx == kNone ? 0.f : exp2f(My - Mx);
     if (partial) {
         const size_t pr = ((size_t)piece * p.T + row) * p.Hq + h;
-        if (d0 == 0) p.part_ml[pr] = make_float2(Mx == kNone ? -INFINITY : Mx, L);
+        if (d0 == 0) p.part_ml[pr] = make_float2(L == 0.f ? -INFINITY : Mx, L);
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
             *reinterpret_cast<float4 *>(p.part_o + pr * 128 + d0 + k) =
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
     }
     if (d0 == 0) {
         if (p.splits > 1) p.part_ml[row * p.Hq + h] = make_float2(0.f, -1.f);
-        p.lse[(size_t)h * p.T + row] = L > 0.f ? (Mx + log2f(L)) * kLn2 : -INFINITY;
+        p.lse[(size_t)h * p.T + row] = L != L ? L : (L > 0.f ? (Mx + log2f(L)) * kLn2 : -INFINITY);
     }
     const float f = L > 0.f ? unit / L : 0.f;                    // a row that sees nothing gives zeros
     uint32_t w[8];

@@ -271,8 +271,9 @@ int hysparse_block_paged(const hs_shape *shape, const int32_t *kv_len, const int
  * max_pages * page_size are below 2^31.
  * HS_E4M3 pools hold 8-bit floats (4 exponent bits, 3 mantissa bits) with one
  * scale byte per row and head in k_scale / v_scale [num_pages][Hkv][page_size]:
- * an element stands for code * 2^(byte - 127).  A power of two makes every
- * such value a bf16 number exactly. */
+ * an element stands for code * 2^(byte - 127), bytes 1 to 254.  A power of
+ * two makes every such value a bf16 number exactly.  Byte 255 marks a row of
+ * NaN, whose codes are all NaN (0x7f or 0xff, which no other row holds). */
 typedef struct {
     const int32_t *cu_rows;       /* DEVICE [B + 1] */
     const int32_t *kv_len;        /* DEVICE [B]: positions in each cache, the new rows' among them */
@@ -308,8 +309,9 @@ int hysparse_rope(int T, int Hq, int Hkv, int d, int dtype, const void *q, long 
  * k, v [T][Hkv][d] of dtype HS_F32 or HS_BF16; d a multiple of 16 up to 256.
  * HS_E4M3 pools get, per row and head, the smallest power of two 2^e with
  * max|x| <= 448 * 2^e (2^0 for a row of zeros, e >= -126) as byte e + 127 and
- * the nearest 8-bit floats (ties to even) of x / 2^e.  Other pool types get x
- * rounded once.  Two rows of one call must not share a pool row.
+ * the nearest 8-bit floats (ties to even) of x / 2^e; a row with a
+ * NaN becomes a row of NaN, and an infinity 448 * 2^120, which widens to
+ * infinity.  Other pool types get x rounded once.  Two rows of one call must not share a pool row.
  * ws (nullable) is only used for its status word.
  * Errors: HS_ERR_INVALID_ARG, HS_ERR_UNSUPPORTED, HS_ERR_CUDA. */
 int hysparse_cache_write(const hs_paged_cache *cache, int T, int Hkv, int d, int dtype, const void *k, long long ld_k,
@@ -342,7 +344,12 @@ size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int 
  * 1/sqrt(d).  max_len: the longest sequence (0: T); a longer one is recorded
  * as HS_ERR_INVALID_ARG and some of its rows are left out.  Rows of no
  * sequence are left as they were.  Probabilities are rounded to bf16 before
- * they meet v; sums are held in fp32.  A wait that gives up
+ * they meet v; sums are held in fp32.  A score that is NaN or +infinity makes
+ * its row's out and lse NaN.  A NaN or infinity in v[j] reaches that column
+ * of the rows that see j (8-bit pools: every column), and may reach it in
+ * rows of the same sequence up to 127 positions before (their probability of
+ * 0 times NaN); no other row.
+ * out must not overlap q, k or v.  A wait that gives up
  * (HS_ERR_TIMEOUT) marks its rows' lse with NaN.
  * ws: 256-byte aligned, hysparse_ragged_workspace_size(B, T, Hq, Hkv, d,
  * max_len, max_len) bytes.

@@ -301,3 +301,40 @@ def test_cache_ops_in_a_graph():
         got = [x.clone() for x in out]
         want = go()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("d", [128, 48])
+@pytest.mark.parametrize("pool", ["bf16", "f32", "e4m3"])
+def test_cache_write_nan_and_infinity(pool, d):
+    """A NaN stays where it is, or (8-bit) makes its row and head one of NaN; an infinity stays, or becomes
+    448 * 2^120 beside codes under that row's scale.  Other rows are not touched by either."""
+    gen = torch.Generator().manual_seed(5)
+    T, Hkv, P = 9, 3, 4
+    k = torch.randn(T, Hkv, d, generator=gen).to(torch.bfloat16)
+    bad = k.clone()
+    bad[2, 1, d - 3] = math.nan
+    bad[4, 0, 7] = math.inf
+    bad[4, 2, 8] = -math.inf
+    bad[7] = math.nan
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    args = (torch.tensor([0, T], dtype=torch.int32, device=DEV), torch.tensor([T], dtype=torch.int32, device=DEV), table)
+    if pool == "e4m3":
+        pools = [torch.zeros(3, P, Hkv, d, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.zeros(3, Hkv, P, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    else:
+        pools = [torch.zeros(3, P, Hkv, d, dtype=DT[pool], device=DEV) for _ in range(2)]
+        scales = [None, None]
+    hs.cache_write(k.to(DEV), bad.to(DEV), *pools, *args, k_scale=scales[0], v_scale=scales[1])
+    clean, got = hs.cache_read(*pools, args[0], table, total=T, k_scale=scales[0], v_scale=scales[1], dtype=torch.float32)
+    clean, got = clean.cpu(), got.cpu()
+    want = clean.clone()
+    if pool == "e4m3":
+        want[2, 1] = math.nan
+        want[4, [0, 2]] = 0.0                             # beside 448 * 2^120, which fp32 has as infinity
+        want[4, 0, 7], want[4, 2, 8] = math.inf, -math.inf
+        assert int((scales[1] == 255).sum()) == 1 + Hkv and int((scales[0] == 255).sum()) == 0
+    else:
+        want[2, 1, d - 3], want[4, 0, 7], want[4, 2, 8] = math.nan, math.inf, -math.inf
+    want[7] = math.nan
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0)) and bool(torch.isfinite(clean).all())

@@ -438,3 +438,63 @@ def test_prompt_in_chunks_then_decode_over_the_same_pages():
         w = ref.attend(dq[b:b + 1].cpu(), rows[0], rows[1], SCALE)
         ref.check_attend(f"chunk {b}", one[b:b + 1], one_lse[:, b:b + 1], w)
         ref.check_attend(f"block {b}", full[b], full_lse[b], w)
+
+
+# ------------------------------------------------------------------ NaN in what is seen
+
+@pytest.mark.parametrize("where", ["k", "q", "v"])
+@pytest.mark.parametrize("new", [[2, 1, 2], [150, 3, 1], [1, 1, 1]])
+@pytest.mark.parametrize("pool", ["bf16", "e4m3", "packed"])
+def test_nan_reaches_the_rows_that_see_it_and_no_others(pool, new, where):
+    """One NaN in sequence 0: a key's makes the rows from its position on NaN, a query's its own row and
+    head, a value's its column (8-bit: all of them) in those rows.  Earlier rows are as ever (but for that column, within a tile),
+    and so are the other sequences'."""
+    gen = torch.Generator().manual_seed(77 + len(where) + sum(new))
+    hq, hkv, P = 8, 2, 16
+    old = [0, 0, 0] if pool == "packed" else [300, 20, 129]
+    kv = [a + b for a, b in zip(new, old)]
+    g, row, head, col = 1, new[0] // 2, 5, 37            # head 5 belongs to KV head 1
+    at = old[0] + row                                    # the position hit
+    T, cu = sum(new), ref.cu_of(new)
+    q = torch.randn(T, hq, 128, generator=gen).to(BF)
+    if pool == "packed":
+        rows = {n: torch.randn(T, hkv, 128, generator=gen).to(BF) for n in "kv"}
+        got = {n: (None, None, [rows[n][int(cu[b]):int(cu[b + 1])].float() for b in range(3)]) for n in "kv"}
+    else:
+        table, got = _paged(gen, kv, P, hkv, pool)
+    qx = q.clone()
+    if where == "q":
+        qx[row, head, col] = math.nan
+    elif pool == "packed":
+        rows[where][at, g, col] = math.nan
+    elif pool == "bf16":
+        got[where][0][int(table[0, at // P]), at % P, g, col] = math.nan
+    else:
+        got[where][0].view(torch.uint8)[int(table[0, at // P]), at % P, g] = 0x7f     # a row of NaN
+        got[where][1][int(table[0, at // P]), g, at % P] = 255
+    if pool == "packed":
+        out, lse = hs.packed_attn(qx.to(DEV), rows["k"].to(DEV), rows["v"].to(DEV), cu.to(DEV), max_len=max(new))
+    else:
+        out, lse = _chunk(qx, got, cu, kv, table, max_q=max(new), max_len=max(kv))
+    out, lse = out.cpu(), lse.cpu()
+    want = [ref.attend(q[int(cu[b]):int(cu[b + 1])], got["k"][2][b], got["v"][2][b], SCALE) for b in range(3)]
+    for b in (1, 2):
+        part = slice(int(cu[b]), int(cu[b + 1]))
+        ref.check_attend(f"seq {b}", out[part], lse[:, part], want[b])
+    n = new[0]
+    heads = [head] if where == "q" else list(range(g * 4, g * 4 + 4))
+    hit = torch.zeros(n, hq, dtype=torch.bool)
+    for h in heads:
+        hit[row:(row + 1 if where == "q" else n), h] = True
+    if where == "v":
+        cols = slice(col, col + 1) if pool != "e4m3" else slice(0, 128)
+        assert bool(torch.isnan(out[:n, :, cols][hit]).all())
+        got_o = out[:n].clone()
+        got_o[:, heads, cols] = want[0][0][:, heads, cols].to(BF)
+        ref.check_attend("other columns", got_o, lse[:, :n], want[0])
+        return
+    assert bool(torch.isnan(out[:n][hit]).all()) and bool(torch.isnan(lse[:, :n].t()[hit]).all())
+    o, l = out[:n].clone(), lse[:, :n].clone()
+    o[hit] = want[0][0][hit].to(BF)
+    l.t()[hit] = want[0][1].t()[hit].float()
+    ref.check_attend("rows that do not see it", o, l, want[0])

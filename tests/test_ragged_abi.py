@@ -143,3 +143,12 @@ def test_chunk_attn_paged_rejects(L):
     need = L.hysparse_ragged_workspace_size(2, 64, 8, 2, 128, 64, 128)
     assert f(max_q=64, wsb=need - 1) == _lib.HS_ERR_WORKSPACE
     assert L.hysparse_chunk_attn_paged(None, 64, 8, 2, 128, 0, 0, 0.0, P(2), 1024, P(5), P(6), P(7), 1 << 30, None) == BAD
+
+
+def test_attention_results_may_not_replace_inputs(L):
+    a = (2, 64, 8, 2, 128, 0, 0.0, P(2), 1024, P(3), 256, P(4), 256)
+    for out in (P(2), P(3), P(4)):
+        assert L.hysparse_packed_attn(P(1), *a, out, P(6), P(7), 1 << 30, None) == BAD
+    c = cache()
+    assert L.hysparse_chunk_attn_paged(ctypes.byref(c), 64, 8, 2, 128, 0, 0, 0.0, P(2), 1024, P(2), P(6), P(7), 1 << 30,
+                                       None) == BAD
