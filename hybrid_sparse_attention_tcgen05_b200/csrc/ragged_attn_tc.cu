@@ -502,6 +502,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         tma_prefetch(&tk);
         tma_prefetch(&tv);
     }
+    Batch batch;
+    if (warp == 11) batch = read_batch(p);       // under the set-up
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -538,9 +540,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         regs_release<R::ctl>();
         if (warp == 11) {
             // ------------------------------------------------ items
-            const Batch bt = read_batch(p);
             for (int i = 0;; ++i) {
-                const Work w = find_work(p, bt, i);
+                const Work w = find_work(p, batch, i);
                 const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->work_empty[i & 1]), ((i >> 1) & 1) ^ 1,
                                                                   p.wait_ns, abort));
                 if (!ok) break;
