@@ -61,7 +61,9 @@ def _build_binding() -> None:
 
     t = os.path.dirname(torch.__file__)
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+    # the g++ that nvcc uses too (not $CXX): one that links its own libstdc++
+    # statically crashes where torch's headers format a message
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
            "-isystem", f"{t}/include", "-isystem", f"{t}/include/torch/csrc/api/include",
            "-isystem", sysconfig.get_paths()["include"],

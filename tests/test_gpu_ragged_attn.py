@@ -498,3 +498,154 @@ def test_nan_reaches_the_rows_that_see_it_and_no_others(pool, new, where):
     o[hit] = want[0][0][hit].to(BF)
     l.t()[hit] = want[0][1].t()[hit].float()
     ref.check_attend("rows that do not see it", o, l, want[0])
+
+
+# ------------------------------------------------------------------ calls at their limits
+
+@pytest.mark.parametrize("pool,new", [("e4m3", [90, 40]), ("e4m3", [20, 12]), ("bf16", [20, 12])])
+def test_wait_limit_marks_lse_of_chunks(monkeypatch, pool, new):
+    """As test_wait_limit_marks_lse, for two row tiles, for one that both warpgroups share, and for 8-bit pages."""
+    gen = torch.Generator().manual_seed(6)
+    kv = [n + 700 for n in new]
+    table, got = _paged(gen, kv, 64, 2, pool)
+    cu, T = ref.cu_of(new), sum(new)
+    q = torch.randn(T, 8, 128, generator=gen).to(BF)
+    ws = torch.zeros(hs.ragged_workspace_size(2, T, 8, 2, 128, max(new), max(kv)), dtype=torch.uint8, device=DEV)
+    monkeypatch.setenv("HYSPARSE_WAIT_LIMIT_NS", "0")
+    _, lse = _chunk(q, got, cu, kv, table, max_q=max(new), max_len=max(kv), ws=ws)
+    assert hs.workspace_status(ws) == _lib.HS_ERR_TIMEOUT and bool(torch.isnan(lse).any())
+    monkeypatch.delenv("HYSPARSE_WAIT_LIMIT_NS")
+    out, lse = _chunk(q, got, cu, kv, table, max_q=max(new), max_len=max(kv), ws=ws)
+    assert hs.workspace_status(ws) == _lib.HS_OK
+    _check_all("after", q, got, cu, new, out, lse)
+
+
+def test_two_threads_call_at_once():
+    """Each on a stream of its own, the library called without the interpreter's lock."""
+    import threading
+    gen = torch.Generator().manual_seed(8)
+    new, old, hq, hkv = [1, 30, 1], [400, 90, 2000], 8, 2
+    kv = [a + b for a, b in zip(new, old)]
+    table, got = _paged(gen, kv, 16, hkv, "e4m3")
+    cu, T = ref.cu_of(new), sum(new)
+    q = [torch.randn(T, hq, 128, generator=gen).to(BF).to(DEV) for _ in range(2)]
+    dcu, dkv, dt = cu.to(DEV), _int(kv), table.to(DEV)
+
+    def go(i):
+        return hs.chunk_attn_paged(q[i], got["k"][0], got["v"][0], dcu, dkv, dt, max_q=max(new), max_len=max(kv),
+                                   k_scale=got["k"][1], v_scale=got["v"][1])
+    want = [go(i) for i in range(2)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(50):
+                out, lse = go(i)
+                st.synchronize()
+                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
+                    bad.append(i)
+                    return
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_pools_past_32_bits(pool):
+    """Pools of more than 2^32 elements, their last and first pages in use."""
+    gen = torch.Generator().manual_seed(9)
+    hq, hkv, P, pages, n = 8, 8, 64, 66000, 300
+    assert pages * P * hkv * 128 > 1 << 32
+    dtype = BF if pool == "bf16" else torch.float8_e4m3fn
+    pk, pv = (torch.empty(pages, P, hkv, 128, dtype=dtype, device=DEV) for _ in range(2))
+    sc = {} if pool == "bf16" else {x: torch.zeros(pages, hkv, P, dtype=torch.uint8, device=DEV)
+                                    for x in ("k_scale", "v_scale")}
+    table = _int([[pages - 1, 0, pages - 2, 65537, pages - 3]])
+    k, v = (torch.randn(n, hkv, 128, generator=gen).to(BF) for _ in range(2))
+    hs.cache_write(k.to(DEV), v.to(DEV), pk, pv, _int([0, n]), _int([n]), table, **sc)
+    bk, bv = (x.cpu() for x in hs.cache_read(pk, pv, _int([0, n]), table, total=n, **sc))
+    for got, x in ((bk, k), (bv, v)):
+        if pool == "bf16":
+            assert torch.equal(got, x)
+        else:
+            codes, byte = ref.e4m3(x.double())
+            assert torch.equal(got.double(), codes * torch.exp2(byte.double() - 127)[..., None])
+    for rows in (1, 5, 100):
+        q = torch.randn(rows, hq, 128, generator=gen).to(BF)
+        out, lse = hs.chunk_attn_paged(q.to(DEV), pk, pv, _int([0, rows]), _int([n]), table, max_q=rows, max_len=n, **sc)
+        ref.check_attend(f"{rows} rows", out, lse, ref.attend(q, bk, bv, SCALE))
+
+
+def test_rows_past_32_bits():
+    """Packed rows of more than 2^31 elements: rotated in place, attended, the last sequences checked."""
+    gen = torch.Generator().manual_seed(10)
+    hq, hkv, n, B = 256, 8, 97, 700
+    T = n * B
+    assert T * hq * 128 > 1 << 31
+    f, _ = hs.rope_frequencies(128, device=DEV)
+    q = torch.zeros(T, hq, 128, dtype=BF, device=DEV)
+    k, v = (torch.zeros(T, hkv, 128, dtype=BF, device=DEV) for _ in range(2))
+    part = slice(T - 2 * n, T)
+    tail = [torch.randn(2 * n, h, 128, generator=gen).to(BF) for h in (hq, hkv, hkv)]
+    for x, y in zip((q, k, v), tail):
+        x[part] = y.to(DEV)
+    pos = torch.arange(n, dtype=torch.int32).repeat(B).to(DEV)
+    wq, wk = hs.rope(q[part].clone(), pos[part].contiguous(), f, k=k[part].clone())
+    hs.rope(q, pos, f, k=k, out=q, out_k=k)
+    assert torch.equal(q[part], wq) and torch.equal(k[part], wk)
+    out, lse = hs.packed_attn(q, k, v, torch.arange(B + 1, dtype=torch.int32, device=DEV) * n, max_len=n)
+    heads = list(range(0, hq, 51))
+    for b in range(2):
+        rows = slice(b * n, (b + 1) * n)
+        want = ref.attend(wq[rows].cpu(), wk[rows].cpu(), tail[2][rows], SCALE)
+        at = slice(T - 2 * n + b * n, T - 2 * n + (b + 1) * n)
+        ref.check_attend(f"seq {B - 2 + b}", out[at][:, heads], lse[heads][:, at],
+                         (want[0][:, heads], want[1][heads], want[2][:, heads]))
+
+
+def test_binding_refusals():
+    """Shapes, types and strides that the calls do not take raise before anything runs."""
+    q, k, v = (torch.zeros(6, h, 128, dtype=BF, device=DEV) for h in (4, 2, 2))
+    cu, kv, table = _int([0, 4, 6]), _int([4, 2]), _int([[0, 1], [2, 3]])
+    pk, pv = (torch.zeros(4, 16, 2, 128, dtype=BF, device=DEV) for _ in range(2))
+    f, _ = hs.rope_frequencies(128, device=DEV)
+    p8, s8 = torch.zeros(4, 16, 2, 128, device=DEV).to(torch.float8_e4m3fn), torch.ones(4, 2, 16, dtype=torch.uint8, device=DEV)
+    pos = _int(list(range(6)))
+    wrong = (TypeError, ValueError)
+    for call in (
+            lambda: hs.rope(q, pos.long(), f), lambda: hs.rope(q, pos[:5], f), lambda: hs.rope(q, pos, f.float()),
+            lambda: hs.rope(q.half(), pos, f), lambda: hs.rope(q[0], pos, f), lambda: hs.rope(q, pos, f, k=k[:5]),
+            lambda: hs.rope(q, pos, f, out=q[:, :2]), lambda: hs.rope(q, pos, f, out_k=k),
+            lambda: hs.rope(q[:, ::2], pos, f), lambda: hs.rope(q[..., :64], pos, f), lambda: hs.rope(q, pos.cpu(), f),
+            lambda: hs.rope(q, pos, f, factor="a"), lambda: hs.rope(None, pos, f),
+            lambda: hs.cache_write(k, v[:5], pk, pv, cu, kv, table), lambda: hs.cache_write(k, v.float(), pk, pv, cu, kv, table),
+            lambda: hs.cache_write(k, v, pk, pv[:3], cu, kv, table), lambda: hs.cache_write(k, v, pk, pv, cu[:2], kv, table),
+            lambda: hs.cache_write(k, v, pk, pv, cu, kv.long(), table), lambda: hs.cache_write(k, v, pk, pv, cu, kv, table[0]),
+            lambda: hs.cache_write(k, v, p8, p8, cu, kv, table), lambda: hs.cache_write(k, v, pk, pv, cu, kv, table, k_scale=s8),
+            lambda: hs.cache_write(k, v, p8, p8, cu, kv, table, k_scale=s8, v_scale=s8[:, :, :8]),
+            lambda: hs.cache_write(k, v, pk.transpose(1, 2), pv.transpose(1, 2), cu, kv, table),
+            lambda: hs.cache_write(k, v, pk, pv, cu, kv, table, ws=torch.zeros(8, device=DEV)),
+            lambda: hs.cache_write(k, v, pk, pv, cu, kv, table, inv_freq=torch.cat([f, f])),
+            lambda: hs.cache_read(pk, pv, cu, table, total=-1), lambda: hs.cache_read(pk, pv, cu, table, total=6, dtype=torch.half),
+            lambda: hs.cache_read(pk, pv, cu, table, total=6, start=_int([0])), lambda: hs.cache_read(pk, pv, cu, table, total=2 ** 40),
+            lambda: hs.cache_read(pk, pv, cu, table, total=6, out_k=torch.zeros(6, 2, 128, device=DEV)),
+            lambda: hs.packed_attn(q.float(), k, v, cu), lambda: hs.packed_attn(q, k.float(), v.float(), cu),
+            lambda: hs.packed_attn(q, k[:5], v[:5], cu), lambda: hs.packed_attn(q, k, v, cu[:1]),
+            lambda: hs.packed_attn(q, k, v, cu, max_len=2 ** 35), lambda: hs.packed_attn(q, k, v, cu, out=q.float()),
+            lambda: hs.packed_attn(q, k, v, cu, lse=torch.zeros(6, 4, device=DEV)), lambda: hs.packed_attn(q, k, v, cu.cpu()),
+            lambda: hs.chunk_attn_paged(q.float(), pk, pv, cu, kv, table), lambda: hs.chunk_attn_paged(q[..., :64], pk, pv, cu, kv, table),
+            lambda: hs.chunk_attn_paged(q, p8, p8, cu, kv, table), lambda: hs.chunk_attn_paged(q, pk, pv, cu, kv[:1], table),
+            lambda: hs.chunk_attn_paged(q, pk, pv, cu, kv, table, out=q[:5])):
+        with pytest.raises(wrong):
+            call()
+    for call in (lambda: hs.packed_attn(q, k, v, cu, out=q), lambda: hs.packed_attn(q, k, v, cu, max_len=-1),
+                 lambda: hs.packed_attn(q, k, v, cu, ws=torch.zeros(256, dtype=torch.uint8, device=DEV)[1:]),
+                 lambda: hs.chunk_attn_paged(q, pk.float(), pv.float(), cu, kv, table),
+                 lambda: hs.rope(q, pos, f, factor=math.inf)):
+        with pytest.raises(hs.HysparseError):
+            call()

@@ -152,3 +152,11 @@ def test_attention_results_may_not_replace_inputs(L):
     c = cache()
     assert L.hysparse_chunk_attn_paged(ctypes.byref(c), 64, 8, 2, 128, 0, 0, 0.0, P(2), 1024, P(2), P(6), P(7), 1 << 30,
                                        None) == BAD
+
+
+def test_binding_shares_the_cpp_runtime(L):
+    """The native binding and torch format messages and throw through one libstdc++: a copy of its own
+    crashed where a refusal prints a shape."""
+    import subprocess
+    needs = subprocess.run(["ldd", hs_build.BINDING], capture_output=True, text=True, check=True).stdout
+    assert "libstdc++" in needs
