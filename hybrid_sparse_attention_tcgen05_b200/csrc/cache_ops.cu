@@ -429,33 +429,35 @@ struct ReadParams {
     void *k, *v;
     unsigned int *status;
     int tokens;
+    int group_shift, dq, dr;       // as in WriteParams
 };
 
-constexpr int kReadTokens = 16;   // most packed rows a block takes
+// Most packed rows a block takes, and rows a thread of it has in flight, of K
+// and of V (24 caches of 16384, e4m3 to bf16, 8 heads: 8 rows and 1, 2, 4 in
+// flight 186, 183, 181 us; 16 rows 188, 186, 183; but 64 elements a head 105,
+// 95, 113.  183 us is 6.4 TB/s, the copy's rate; with 16 elements a thread,
+// whose two stores each fill half of a 32-byte sector, it was 208).
+constexpr int kReadTokens = 8, kReadBatch = 2;
 
-// Sixteen elements of a cache row as floats (the row's power of two applied).
-template <typename TC>
-__device__ __forceinline__ void widen16(const TC *p, float, float (&x)[16]) {
-    float a[8], b[8];
-    load_n<8>(p, a);
-    load_n<8>(p + 8, b);
+// Eight neighbouring elements of a cache row and its scale.
+template <typename TC> struct CacheRaw8 : Raw8<TC> {
+    __device__ __forceinline__ void widen_scaled(float (&x)[8], float) const { this->widen(x); }
+};
+template <> struct CacheRaw8<__nv_fp8_e4m3> {
+    uint2 q;
+    __device__ __forceinline__ void load(const __nv_fp8_e4m3 *p) { q = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void widen_scaled(float (&x)[8], float scale) const {
+        const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = a[i];
-        x[8 + i] = b[i];
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h =
+                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            x[2 * i] = f.x * scale;
+            x[2 * i + 1] = f.y * scale;
+        }
     }
-}
-__device__ __forceinline__ void widen16(const __nv_fp8_e4m3 *p, float scale, float (&x)[16]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        x[2 * i] = f.x * scale;
-        x[2 * i + 1] = f.y * scale;
-    }
-}
+};
 
 template <typename TC, typename TO, bool Q8>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p) {
@@ -475,35 +477,44 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
         if (lane == 0) slot[i] = r;
     }
     __syncthreads();
-    const int units = p.d / 16;
-    const int n = nt * p.Hkv * units;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int tok = i / (p.Hkv * units);
-        const int rest = i - tok * p.Hkv * units;
-        const int h = rest / units, e0 = (rest - h * units) * 16;
-        const long long r = slot[tok];
-        if (r < 0) continue;
-        const size_t src = ((size_t)r * p.Hkv + h) * p.d + e0;
-        const size_t dst = ((size_t)(t0 + tok) * p.Hkv + h) * p.d + e0;
-        float ks = 1.f, vs = 1.f;
-        if (Q8) {
-            const size_t si = scale_index(p.c, r, p.Hkv, h);
-            ks = scale_of_byte(p.c.k_scale[si]);
-            vs = scale_of_byte(p.c.v_scale[si]);
-        }
-        float x[16], y[16];
-        widen16((const TC *)p.c.k_pages + src, ks, x);
-        widen16((const TC *)p.c.v_pages + src, vs, y);
-        float a[8], b[8];
+    // one group of lanes per (token, head) row of K and of V, eight elements a lane
+    const int group = 1 << p.group_shift, sub = threadIdx.x & (group - 1);
+    int tok = (int)(threadIdx.x >> p.group_shift) / p.Hkv, h = (int)(threadIdx.x >> p.group_shift) - tok * p.Hkv;
+    while (tok < nt) {
+        CacheRaw8<TC> k[kReadBatch], v[kReadBatch];
+        int kb[kReadBatch], vb[kReadBatch];
+        size_t dst[kReadBatch];
+        bool live[kReadBatch];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                a[e] = x[8 * half + e];
-                b[e] = y[8 * half + e];
+        for (int u = 0; u < kReadBatch; ++u) {
+            const long long r = tok < nt ? slot[tok] : -1;
+            live[u] = r >= 0 && sub * 8 < p.d;
+            dst[u] = ((size_t)(t0 + tok) * p.Hkv + h) * p.d + sub * 8;
+            if (live[u]) {
+                const size_t src = ((size_t)r * p.Hkv + h) * p.d + sub * 8;
+                k[u].load((const TC *)p.c.k_pages + src);
+                v[u].load((const TC *)p.c.v_pages + src);
+                if (Q8) {
+                    const size_t si = scale_index(p.c, r, p.Hkv, h);
+                    kb[u] = p.c.k_scale[si];
+                    vb[u] = p.c.v_scale[si];
+                }
             }
-            store_n<8>((TO *)p.k + dst + 8 * half, a);
-            store_n<8>((TO *)p.v + dst + 8 * half, b);
+            tok += p.dq;
+            h += p.dr;
+            if (h >= p.Hkv) {
+                h -= p.Hkv;
+                ++tok;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kReadBatch; ++u) {
+            if (!live[u]) continue;
+            float x[8];
+            k[u].widen_scaled(x, Q8 ? scale_of_byte(kb[u]) : 1.f);
+            store_n<8>((TO *)p.k + dst[u], x);
+            v[u].widen_scaled(x, Q8 ? scale_of_byte(vb[u]) : 1.f);
+            store_n<8>((TO *)p.v + dst[u], x);
         }
     }
 }
@@ -511,6 +522,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
 template <typename TC, typename TO, bool Q8>
 cudaError_t read_go(ReadParams p, cudaStream_t st) {
     p.tokens = p.total >= 8192 ? kReadTokens : (p.total >= 1024 ? 4 : 1);
+    p.group_shift = 0;
+    while ((8 << p.group_shift) < p.d) ++p.group_shift;
+    p.dq = (kThreads >> p.group_shift) / p.Hkv;
+    p.dr = (kThreads >> p.group_shift) % p.Hkv;
     cache_read_kernel<TC, TO, Q8><<<(p.total + p.tokens - 1) / p.tokens, kThreads, 0, st>>>(p);
     count_launch();
     return cudaGetLastError();
@@ -549,7 +564,7 @@ cudaError_t cache_write_launch(const PagedCache &c, int T, int Hkv, int d, int d
 
 cudaError_t cache_read_launch(const PagedCache &c, const int32_t *start, int total, int Hkv, int d, int dtype,
                               void *k, void *v, unsigned int *status, cudaStream_t st) {
-    ReadParams p{c, start, total, Hkv, d, k, v, status, 1};
+    ReadParams p{c, start, total, Hkv, d, k, v, status, 1, 0, 0, 0};
     if (dtype == HS_F32) {
         if (c.dtype == HS_E4M3) return read_go<__nv_fp8_e4m3, float, true>(p, st);
         if (c.dtype == HS_BF16) return read_go<__nv_bfloat16, float, false>(p, st);
