@@ -29,102 +29,128 @@ struct RopeParams {
     int inverse;
     int units;      // units of one row that need work (pairs, and the part left as it is when it has to be copied)
     int tokens;     // tokens a block takes
+    int dt, dh, du; // what a thread's next unit is further: tokens, heads, units
 };
+
+// Units a thread has in flight (65536 tokens of 68 heads, bf16: one 365 us, two
+// 362, three 378, four 377; the part of 64 of their 128 elements 423, 402, 422,
+// 413).  362 us is 6.3 TB/s, 0.96 of the copy's rate; with the units' places by
+// division and the angles before the first loads it was 409 and 696.
+constexpr int kRopeBatch = 2;
+
+// As many bytes as they lie in memory.
+template <int N> struct RawBytes;
+template <> struct RawBytes<16> { uint4 q; };
+template <> struct RawBytes<8> { uint2 q; };
+template <> struct RawBytes<4> { uint32_t q; };
+template <> struct RawBytes<2> { uint16_t q; };
 
 // One unit of a row: V pairs (first and second halves: 2 V elements) or V
 // neighbouring elements (V / 2 pairs), or V elements that are only copied.
 template <typename T, int V, bool INTER>
 struct RopeUnit {
-    float a[V], b[V];
-    const T *src;
-    T *dst;
-    int pair;       // first pair of the unit, < 0: copy
-    __device__ void load(const RopeParams &p, int t, int head, int u) {
+    using Raw = RawBytes<V * (int)sizeof(T)>;
+    Raw a, b;
+    T *dst;         // null: no unit
+    int cs;         // its first pair's angles, < 0: copy
+    __device__ void load(const RopeParams &p, int t0, int tok, int head, int u) {
+        const long long t = t0 + tok;
+        const T *src;
         if (head < p.Hq) {
-            src = (const T *)p.q + t * p.ld_q + (long long)head * p.d;
-            dst = (T *)p.oq + t * p.ld_oq + (long long)head * p.d;
+            src = (const T *)p.q + t * p.ld_q + head * p.d;
+            dst = (T *)p.oq + t * p.ld_oq + head * p.d;
         } else {
-            src = (const T *)p.k + t * p.ld_k + (long long)(head - p.Hq) * p.d;
-            dst = (T *)p.ok + t * p.ld_ok + (long long)(head - p.Hq) * p.d;
+            src = (const T *)p.k + t * p.ld_k + (head - p.Hq) * p.d;
+            dst = (T *)p.ok + t * p.ld_ok + (head - p.Hq) * p.d;
         }
-        const int at = u * V;
-        if (INTER) {
-            pair = at < 2 * p.half ? at / 2 : -1;
-            src += at;
-            dst += at;
-            load_n<V>(src, a);
-        } else if (at < p.half) {
-            pair = at;
-            src += at;
-            dst += at;
-            load_n<V>(src, a);
-            load_n<V>(src + p.half, b);
-        } else {
-            pair = -1;
-            src += at + p.half;   // units from half / V on are the rest, elements 2 * half ..
-            dst += at + p.half;
-            load_n<V>(src, a);
-        }
+        int at = u * V;
+        const bool turned = at < (INTER ? 2 * p.half : p.half);
+        cs = turned ? tok * p.half + (INTER ? at / 2 : at) : -1;
+        if (!INTER && !turned) at += p.half;   // units from half / V on are the rest, elements 2 * half ..
+        a = *reinterpret_cast<const Raw *>(src + at);
+        if (!INTER && turned) b = *reinterpret_cast<const Raw *>(src + at + p.half);
+        dst += at;
     }
-    __device__ void store(const RopeParams &p, const float2 *cs) {
-        if (pair >= 0) {
-            if (INTER) {
+    static __device__ void widen(const Raw &r, float (&x)[V]) {
+        const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
-                for (int e = 0; e + 1 < V; e += 2) {
-                    const float2 w = cs[pair + e / 2];
-                    const float x = a[e], y = a[e + 1];
-                    a[e] = rope_first(x, y, w);
-                    a[e + 1] = rope_second(x, y, w);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float2 w = cs[pair + e];
-                    const float x = a[e], y = b[e];
-                    a[e] = rope_first(x, y, w);
-                    b[e] = rope_second(x, y, w);
-                }
-                store_n<V>(dst + p.half, b);
-            }
+        for (int i = 0; i < V; ++i) x[i] = Elem<T>::to_f(e[i]);
+    }
+    __device__ void store(const RopeParams &p, const float2 *angles) const {
+        if (cs < 0) {
+            *reinterpret_cast<Raw *>(dst) = a;
+            return;
         }
-        store_n<V>(dst, a);
+        float x[V], y[V];
+        widen(a, x);
+        const float2 *w = angles + cs;
+        if (INTER) {
+#pragma unroll
+            for (int e = 0; e + 1 < V; e += 2) {
+                const float f = x[e], g = x[e + 1];
+                x[e] = rope_first(f, g, w[e / 2]);
+                x[e + 1] = rope_second(f, g, w[e / 2]);
+            }
+        } else {
+            widen(b, y);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float f = x[e], g = y[e];
+                x[e] = rope_first(f, g, w[e]);
+                y[e] = rope_second(f, g, w[e]);
+            }
+            store_n<V>(dst + p.half, y);
+        }
+        store_n<V>(dst, x);
     }
 };
 
 // The angles depend on the token and the pair only, so a block computes them
 // once for its tokens (in 64 bits, into shared memory) and turns all the
-// heads of q and k with them.  A unit is read whole before any of it is
-// written, so out may be the input itself.
+// heads of q and k with them; a thread's first units are asked for before
+// that.  A unit is read whole before any of it is written, so out may be the
+// input itself.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     extern __shared__ float2 cs[];
     const int t0 = blockIdx.x * p.tokens;
     const int nt = min(p.tokens, p.T - t0);
-    for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
-        float2 w = rope_cs(__ldg(p.positions + t0 + i / p.half), p.inv_freq[i % p.half], p.amp);
-        if (p.inverse) w.y = -w.y;
-        cs[i] = w;
-    }
-    __syncthreads();
-    const int per_token = (p.Hq + p.Hkv) * p.units;
-    const int n = nt * per_token;
-    constexpr int BATCH = 2;
-    for (int i0 = (blockIdx.y * BATCH) * kThreads + threadIdx.x; i0 < n; i0 += BATCH * kThreads * gridDim.y) {
-        RopeUnit<T, V, INTER> w[BATCH];
-        int tok[BATCH];
+    const int heads = p.Hq + p.Hkv;
+    // this thread's next unit: one division, then steps
+    const int i0 = blockIdx.y * kThreads + threadIdx.x;
+    int u = i0 % p.units, head = i0 / p.units, tok = head / heads;
+    head -= tok * heads;
+    RopeUnit<T, V, INTER> w[kRopeBatch];
+    auto ask = [&]() {
 #pragma unroll
-        for (int e = 0; e < BATCH; ++e) {
-            const int i = i0 + e * kThreads;
-            tok[e] = -1;
-            if (i < n) {
-                tok[e] = i / per_token;
-                const int r = i - tok[e] * per_token;
-                w[e].load(p, t0 + tok[e], r / p.units, r % p.units);
+        for (int e = 0; e < kRopeBatch; ++e) {
+            w[e].dst = nullptr;
+            if (tok < nt) w[e].load(p, t0, tok, head, u);
+            u += p.du;
+            head += p.dh;
+            tok += p.dt;
+            if (u >= p.units) {
+                u -= p.units;
+                ++head;
+            }
+            if (head >= heads) {
+                head -= heads;
+                ++tok;
             }
         }
+    };
+    ask();
+    for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
+        float2 v = rope_cs(__ldg(p.positions + t0 + i / p.half), p.inv_freq[i % p.half], p.amp);
+        if (p.inverse) v.y = -v.y;
+        cs[i] = v;
+    }
+    __syncthreads();
+    while (w[0].dst != nullptr) {
 #pragma unroll
-        for (int e = 0; e < BATCH; ++e)
-            if (tok[e] >= 0) w[e].store(p, cs + tok[e] * p.half);
+        for (int e = 0; e < kRopeBatch; ++e)
+            if (w[e].dst != nullptr) w[e].store(p, cs);
+        ask();
     }
 }
 
@@ -134,13 +160,17 @@ cudaError_t rope_go(RopeParams p, bool copy_rest, cudaStream_t st) {
     const long long per_token = (long long)(p.Hq + p.Hkv) * p.units;
     // one token a block while that leaves SMs idle, then eight: fewer blocks,
     // and the angles of eight tokens fill the block's threads (65536 tokens of
-    // 68 heads: two 477 us, four 429, eight 416)
+    // 68 heads: four 374 us, eight 362)
     p.tokens = p.T >= 4096 ? 8 : 1;
     const int blocks = (p.T + p.tokens - 1) / p.tokens;
     const long long n = per_token * p.tokens;
     int y = (int)((n + 2 * kThreads - 1) / (2 * kThreads));
     if (blocks >= 592) y = 1;          // four blocks an SM: the heads need no further split
     y = y < 1 ? 1 : (y > 8 ? 8 : y);
+    const int step = kThreads * y;
+    p.dt = (int)(step / per_token);
+    p.dh = (int)(step % per_token) / p.units;
+    p.du = (int)(step % per_token) % p.units;
     rope_kernel<T, V, INTER><<<dim3(blocks, y), kThreads, p.tokens * p.half * sizeof(float2), st>>>(p);
     count_launch();
     return cudaGetLastError();
