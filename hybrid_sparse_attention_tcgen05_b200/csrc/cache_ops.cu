@@ -301,6 +301,7 @@ __device__ __forceinline__ int scale_byte(float amax) {
 
 constexpr int kBatch = 4;          // rows a thread of the write has in flight
 constexpr int kWriteTokens = 8;    // most tokens a block of it takes
+static_assert(kWriteTokens <= kThreads / 32, "a warp finds each token's place");
 
 // One group of lanes per (token, K or V, head) row, eight elements a lane.
 // 8-bit rows: the group's largest magnitude gives the scale, a power of two,
