@@ -54,6 +54,7 @@ namespace {
 
 constexpr int kStage = TILE / 2;       // one 128-key tile of 8-bit rows: 16 KB
 constexpr int kBadBufs = 8;
+constexpr int kMaxSplits = 64;         // pieces of a row at most
 
 // Shared memory: Q0, Q1, four K/V tiles (for 8-bit caches three, and two
 // staged 8-bit tiles), and 4 KB for each softmax warp's results on their way
@@ -1169,34 +1170,47 @@ __global__ void __launch_bounds__(256) ragged_combine(const RaggedParams p) {
     const long long rows = (long long)p.T * p.Hq;
     if (r >= rows) return;
     const int t = (int)(r / p.Hq), h = (int)(r - (long long)t * p.Hq);
+    // everything is asked for at once: two pieces' maximum and sum a lane, O of
+    // the first eight pieces (what an empty piece left there is not used)
+    static_assert(kMaxSplits <= 64, "two pieces a lane");
+    float2 ml[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        ml[i] = lane + 32 * i < p.splits ? p.part_ml[(lane + 32 * i) * rows + r] : make_float2(-INFINITY, 0.f);
+    const float *const src = p.part_o + r * HD + lane * 4;
+    float4 o[8];
+    auto ask = [&](int s0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (s0 + j < p.splits) o[j] = __ldcg(reinterpret_cast<const float4 *>(src + (s0 + j) * rows * HD));
+    };
+    ask(0);
     if (t < clamp_row(__ldg(p.c.cu_rows), p.T) || t >= clamp_row(__ldg(p.c.cu_rows + p.c.B), p.T)) return;
-    if (p.part_ml[r].y < 0.f) return;                       // written by its only piece
-    float m = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_ml[s * rows + r].x);
-    m = warp_max(m);
-    float l = 0.f;
+    if (__shfl_sync(0xffffffffu, ml[0].y, 0) < 0.f) return;   // written by its only piece
+    const float m = warp_max(fmaxf(ml[0].x, ml[1].x));
+    // each piece's weight, 0 when it saw nothing (its O was not written then);
+    // NaN of a piece that gave up carries through
+    float a[2], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        a[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - m);
+        l += ml[i].x == -INFINITY ? 0.f : a[i] * ml[i].y;
+    }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < p.splits; s0 += 32) {
-        // one piece a lane: its weight, 0 when it saw nothing (its O was not
-        // written then); NaN of a piece that gave up carries through
-        float a = 0.f;
-        if (s0 + lane < p.splits) {
-            const float2 ml = p.part_ml[(s0 + lane) * rows + r];
-            a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-            l += ml.x == -INFINITY ? 0.f : a * ml.y;
+    for (int s0 = 0;;) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = __shfl_sync(0xffffffffu, s0 < 32 ? a[0] : a[1], (s0 + j) & 31);
+            if (s0 + j < p.splits && f != 0.f) {
+                acc.x += f * o[j].x;
+                acc.y += f * o[j].y;
+                acc.z += f * o[j].z;
+                acc.w += f * o[j].w;
+            }
         }
-        const int n = min(32, p.splits - s0);
-        const float *src = p.part_o + (s0 * rows + r) * HD + lane * 4;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) {
-            const float f = __shfl_sync(0xffffffffu, a, j);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (f != 0.f) o = *reinterpret_cast<const float4 *>(src + j * rows * HD);
-            acc.x += f * o.x;
-            acc.y += f * o.y;
-            acc.z += f * o.z;
-            acc.w += f * o.w;
-        }
+        s0 += 8;
+        if (s0 >= p.splits) break;
+        ask(s0);
     }
     l = warp_sum(l);
     const float inv = l > 0.f ? 1.f / l : (l != l ? l : 0.f);
@@ -1255,7 +1269,6 @@ cudaError_t prepare() {
 }
 
 constexpr int kSms = 148;
-constexpr int kMaxSplits = 64;
 // Rows (new tokens x group) a sequence up to which the warp-MMA kernel runs.
 // Measured with 32 / 8 heads, 16 caches of 8192, 64 of 2048 (us; 8, 16, 32, 64
 // rows): bf16 91, 91, 118, 233 against 120 of the tcgen05 kernel, and 87, 91,
