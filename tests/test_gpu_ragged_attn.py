@@ -649,3 +649,26 @@ def test_binding_refusals():
                  lambda: hs.rope(q, pos, f, factor=math.inf)):
         with pytest.raises(hs.HysparseError):
             call()
+
+
+def test_no_rows():
+    """Batches of no rows at all, and of sequences without rows."""
+    q, k = torch.zeros(0, 4, 128, dtype=BF, device=DEV), torch.zeros(0, 2, 128, dtype=BF, device=DEV)
+    pk, pv = (torch.full((3, 16, 2, 128), 5.0, dtype=BF, device=DEV) for _ in range(2))
+    cu, kv, table = _int([0, 0, 0]), _int([0, 7]), _int([[0], [1]])
+    f, _ = hs.rope_frequencies(128, device=DEV)
+    rq, rk = hs.rope(q, _int([]), f, k=k)
+    assert rq.shape == q.shape and rk.shape == k.shape
+    hs.cache_write(k, k, pk, pv, cu, kv, table, inv_freq=f)
+    back = hs.cache_read(pk, pv, cu, table, total=0)
+    assert back[0].shape == (0, 2, 128)
+    for out, lse in (hs.packed_attn(q, k, k, cu), hs.chunk_attn_paged(q, pk, pv, cu, kv, table)):
+        assert out.shape == q.shape and lse.shape == (4, 0)
+    # rows that belong to no sequence only
+    q, k = torch.zeros(9, 4, 128, dtype=BF, device=DEV), torch.zeros(9, 2, 128, dtype=BF, device=DEV)
+    out, lse = torch.full_like(q, 3.0), torch.full((4, 9), 3.0, device=DEV)
+    hs.cache_write(k, k, pk, pv, cu, kv, table, inv_freq=f)
+    for most in (1, 9):
+        hs.chunk_attn_paged(q, pk, pv, cu, kv, table, max_q=most, out=out, lse=lse)
+    hs.packed_attn(q, k, k, cu, out=out, lse=lse)
+    assert bool((pk == 5).all()) and bool((out == 3).all()) and bool((lse == 3).all())
