@@ -838,12 +838,21 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const uint8_t *src = sst + st.slot * kStage + r0 * 128 + c16 * 16;
                     uint8_t *dst = skv + kv.slot * TILE;
                     // rows that are not there keep finite leftovers: their probabilities are exactly 0
-#pragma unroll 4
+                    // four rows' codes are read before the first of them is stored: the
+                    // compiler cannot move a read over a store to the same memory
+                    uint2 u[4], v[4];
+                    uint32_t scales[4];
+#pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(src + i * 2048 + first * 8);
-                        const uint2 v = *reinterpret_cast<const uint2 *>(src + i * 2048 + 8 - first * 8);
-                        const uint32_t sb = bars->scale[buf][r0 + 16 * i];
-                        const uint32_t w[4] = {u.x, u.y, v.x, v.y};
+                        if ((i & 3) == 0)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                u[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + first * 8);
+                                v[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + 8 - first * 8);
+                                scales[k] = bars->scale[buf][r0 + 16 * (i + k)];
+                            }
+                        const uint32_t sb = scales[i & 3];
+                        const uint32_t w[4] = {u[i & 3].x, u[i & 3].y, v[i & 3].x, v[i & 3].y};
                         uint32_t o[8];
                         // 2^(120 + byte - 127) as a bf16 pair, up to 2^127
                         uint32_t f = min(sb, 134u) * 0x00800080u + 0x3c003c00u;
