@@ -1281,8 +1281,8 @@ constexpr int kSms = 148;
 // Rows (new tokens x group) a sequence up to which the warp-MMA kernel runs.
 // Measured with 32 / 8 heads, 16 caches of 8192, 64 of 2048 (us; 8, 16, 32, 64
 // rows): bf16 82, 84, 110, 215 against 111 of the tcgen05 kernel, and 83, 87,
-// 138, 210 against 127; 8-bit 53, 70, 130, 255 against 195, and 70, 99, 147,
-// 232 against 211.
+// 138, 210 against 127; 8-bit 53, 70, 130, 255 against 182, and 70, 99, 147,
+// 232 against 208.
 constexpr int kFewRows16 = 16, kFewRows8 = 32;
 constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an SM holds (bf16, 8-bit caches)
 constexpr int kFewRowsFixed = 16;          // what a piece costs besides its keys, in 16-key blocks
