@@ -27,6 +27,8 @@
 //   11        finds the items, two ahead
 //   12-15     8-bit caches only: widen staged rows to bf16 tiles.  A code
 //             times a power of two is a bf16 number, so nothing is rounded.
+//             Their instructions are what bounds 8-bit chunks (441 us for 4 of
+//             1000 over 12000, 374 with bf16 pages).
 // TMEM (512 columns): two S buffers of 64 keys for each row tile, then O0 and
 // O1.  A key tile is taken in two steps of 64 keys, so that S of the next step
 // is computed while the softmax of this one runs: with one 128-key S per row
@@ -96,7 +98,7 @@ struct RaggedBars {
     int abort;
     uint32_t bad_any[kBadBufs];           // K tile i of the CTA has keys on pages outside the pool: bad[i % 8] says which
     uint32_t bad[kBadBufs][4];
-    uint8_t scale[2][128];                // 8-bit caches: scale bytes of the tile being widened
+    uint8_t scale[2][128];                // scale bytes of the staged tiles
     float2 side[128];                     // solo: warpgroup 1's maximum and sum of each row
     Work work[2];
 };
@@ -318,18 +320,6 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Named barrier 2 over 128 threads; whether all of them said yes.
-__device__ __forceinline__ bool all_128(bool yes) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)yes)
-        : "memory");
-    return r != 0;
-}
-
 // One lane of the warp, the same each time.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
@@ -451,6 +441,40 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
 // prompt, 64/4 heads: none 1008 us, two 975, four 1020).
 constexpr int kFmaPairs = 2;
 
+// The scale bytes of keys key0 + 4 * lane .. + 3 of a tile to `to` (one warp);
+// 0 for a row that is not there, whose leftovers in the stage become next to
+// nothing then.  page: lane i has the page of the tile's i-th box.  Their
+// arrival counts on the tile's barrier: nobody waits for them here.  (Looked
+// up by the converters a tile ahead, they cost an eighth of the whole: 512 us
+// for 4 chunks of 1000 over 12000 cached, here 441.)
+__device__ __forceinline__ void load_scales(const RaggedParams &p, const Work &wk, const int32_t *table, int page,
+                                            int rshift, int key0, bool is_v, uint8_t *to, uint32_t bar) {
+    const int lane = threadIdx.x & 31;
+    const int key = key0 + 4 * lane, mask = (1 << p.c.page_shift) - 1;
+    const uint8_t *const scales = is_v ? p.c.v_scale : p.c.k_scale;
+    if (p.c.page_shift >= 2) {
+        const int pg = __shfl_sync(0xffffffffu, page, (4 * lane) >> rshift);
+        int n = min(max(wk.kvl - key, 0), 4);
+        if (pg < 0 || pg >= p.c.num_pages) n = 0;
+        const size_t at = n > 0 ? (((size_t)pg * p.Hkv + wk.g) << p.c.page_shift) + (key & mask) : 0;
+        asm volatile(
+            "cp.async.ca.shared.global [%0], [%1], 4, %2;\n\t"
+            "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%3];" ::"r"(smem_u32(to)),
+            "l"(scales + at), "r"(n), "r"(bar)
+            : "memory");
+        return;
+    }
+    uint32_t bytes = 0;                        // pages of one and two rows
+    for (int r = 0; r < 4; ++r) {
+        if (key + r >= wk.kvl) break;
+        const int pg = __ldg(table + ((key + r) >> p.c.page_shift));
+        if (pg >= 0 && pg < p.c.num_pages)
+            bytes |= (uint32_t)__ldg(scales + (((size_t)pg * p.Hkv + wk.g) << p.c.page_shift) + ((key + r) & mask)) << (8 * r);
+    }
+    *reinterpret_cast<uint32_t *>(to) = bytes;
+    mbar_arrive(bar);
+}
+
 template <bool F8>
 __global__ void __launch_bounds__(Ring<F8>::threads, 1)
 ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -474,7 +498,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             mbar_init(smem_u32(&bars->kv_empty[s]), 2);
         }
         for (int s = 0; s < 4; ++s) {
-            mbar_init(smem_u32(&bars->st_full[s]), 1);
+            mbar_init(smem_u32(&bars->st_full[s]), 1 + 32);     // the tile; each lane's scales
             mbar_init(smem_u32(&bars->st_empty[s]), 128);
         }
         for (int w = 0; w < 2; ++w) {
@@ -624,6 +648,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         for (int hf = 0; hf < parts; ++hf)
                             tma_load_4d(dst + hf * HALF + (i << rshift) * row_bytes, m, fb, hf * 64, wk.g, c2, c3);
                     }
+                    if constexpr (F8) load_scales(p, wk, table, page, rshift, key0, is_v, &bars->scale[pos.slot][4 * lane], fb);
                     ++issued;
                     pos.next(slots);
                 }
@@ -803,37 +828,13 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const uint32_t at0 = row_at + ((((2 * c16) & 7) + first) ^ (r0 & 7)) * 16;
             const uint32_t at1 = row_at + ((((2 * c16) & 7) + 1 - first) ^ (r0 & 7)) * 16;
             RingPos st, kv;
-            uint32_t tiles = 0;
             bool ok = true;
-            while (all_128(ok && next_work())) {     // the four warps go on, or leave, together
+            while (ok && next_work()) {
                 const int n = wk.n;
-                const bool solo = wk.solo != 0;
-                const int32_t *table = p.c.block_table + (size_t)wk.b * p.c.max_pages;
-                // scale byte of this thread's row (t) of item `it`; 0: no such row (it becomes zeros)
-                auto scale_load = [&](int it) -> int {
-                    if (it >= 2 * n) return 0;
-                    int j;
-                    bool is_v;
-                    kv_item(it, n, solo, j, is_v);
-                    const int key = (wk.j0 + j) * BN + t;
-                    if (key >= wk.kvl) return 0;
-                    const int page = __ldg(table + (key >> p.c.page_shift));
-                    if (page < 0 || page >= p.c.num_pages) return 0;
-                    const uint8_t *s = is_v ? p.c.v_scale : p.c.k_scale;
-                    return __ldg(s + (((size_t)page * p.Hkv + wk.g) << p.c.page_shift) +
-                                 (key & ((1 << p.c.page_shift) - 1)));
-                };
-                int byte = scale_load(0);
-                for (int it = 0; it < 2 * n; ++it, ++tiles) {
-                    const int buf = tiles & 1;
-                    bars->scale[buf][t] = (uint8_t)byte;
-                    byte = scale_load(it + 1);
+                for (int it = 0; it < 2 * n; ++it) {
                     ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->st_full[st.slot]), st.phase, p.wait_ns, abort));
                     ok = ok && __all_sync(0xffffffffu, bar_wait(smem_u32(&bars->kv_empty[kv.slot]), kv.phase ^ 1,
                                                                  p.wait_ns, abort));
-                    // the four warps meet here for the scale bytes, and leave together when
-                    // one of them gave up waiting
-                    ok = all_128(ok);
                     if (!ok) break;
                     const uint8_t *src = sst + st.slot * kStage + r0 * 128 + c16 * 16;
                     uint8_t *dst = skv + kv.slot * TILE;
@@ -849,7 +850,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                             for (int k = 0; k < 4; ++k) {
                                 u[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + first * 8);
                                 v[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + 8 - first * 8);
-                                scales[k] = bars->scale[buf][r0 + 16 * (i + k)];
+                                scales[k] = bars->scale[st.slot][r0 + 16 * (i + k)];
                             }
                         const uint32_t sb = scales[i & 3];
                         const uint32_t w[4] = {u[i & 3].x, u[i & 3].y, v[i & 3].x, v[i & 3].y};
@@ -1281,8 +1282,8 @@ constexpr int kSms = 148;
 // Rows (new tokens x group) a sequence up to which the warp-MMA kernel runs.
 // Measured with 32 / 8 heads, 16 caches of 8192, 64 of 2048 (us; 8, 16, 32, 64
 // rows): bf16 82, 84, 110, 215 against 111 of the tcgen05 kernel, and 83, 87,
-// 138, 210 against 127; 8-bit 53, 70, 130, 255 against 182, and 70, 99, 147,
-// 232 against 208.
+// 138, 210 against 127; 8-bit 53, 70, 130, 255 against 157, and 70, 99, 147,
+// 232 against 186.
 constexpr int kFewRows16 = 16, kFewRows8 = 32;
 constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an SM holds (bf16, 8-bit caches)
 constexpr int kFewRowsFixed = 16;          // what a piece costs besides its keys, in 16-key blocks
