@@ -1,8 +1,11 @@
 // The memory-bound operators around the attention calls: rotary positions,
 // the write of new keys and values into paged caches (copied, or as 8-bit
 // floats under a power-of-two scale per row and head) and its counterpart
-// that reads rows back.  All three are bound by HBM: each input byte is read
-// once and each output byte written once, in 16-byte accesses.
+// that reads rows back.  Each input byte is read once and each output byte
+// written once, in 16-byte accesses.  Rope and the read run at the copy's rate
+// (6.3 and 6.4 TB/s); the write does copied (16959 tokens of 8 heads 25.7 us,
+// 5.4 TB/s), but turning (37 us), 8-bit rows (34 us) or both (46 us) are bound
+// by instructions and by the chains of shuffles.
 #include <atomic>
 
 #include <cuda_bf16.h>

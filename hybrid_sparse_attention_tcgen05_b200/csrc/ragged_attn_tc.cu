@@ -64,6 +64,7 @@ constexpr int kMaxSplits = 64;         // pieces of a row at most
 template <bool F8> struct Ring {
     static constexpr int slots = F8 ? 3 : 4;
     static constexpr int stages = F8 ? 2 : 0;
+    static_assert(slots <= 4 && stages <= 2, "RaggedBars");
     static constexpr int threads = F8 ? 512 : 384;
     // launch registers and shares after the hand-over (setmaxnreg): the
     // shares add up to at most what the block was launched with
@@ -86,8 +87,8 @@ struct Work {
 
 struct RaggedBars {
     uint64_t q_full, q_empty;             // q_empty: the MMAs have read Q (commit), and a warpgroup has no use for its place
-    uint64_t kv_full[5], kv_empty[5];
-    uint64_t st_full[4], st_empty[4];     // staged 8-bit tiles
+    uint64_t kv_full[4], kv_empty[4];     // K/V tiles (Ring::slots of them)
+    uint64_t st_full[2], st_empty[2];     // staged 8-bit tiles
     uint64_t s_full[2][2], p_full[2][2];  // of each S buffer
     uint64_t pv_done[2];                  // each step's P V
     uint64_t o_full[2], o_empty[2];       // an item's last P V; O read out
@@ -493,11 +494,11 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->q_full), 1);
         mbar_init(smem_u32(&bars->q_empty), 2 + 128);
-        for (int s = 0; s < 5; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(smem_u32(&bars->kv_full[s]), F8 ? 128 : 1);
             mbar_init(smem_u32(&bars->kv_empty[s]), 2);
         }
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars->st_full[s]), 1 + 32);     // the tile; each lane's scales
             mbar_init(smem_u32(&bars->st_empty[s]), 128);
         }
