@@ -27,8 +27,8 @@
 //   11        finds the items, two ahead
 //   12-15     8-bit caches only: widen staged rows to bf16 tiles.  A code
 //             times a power of two is a bf16 number, so nothing is rounded.
-//             Their instructions are what bounds 8-bit chunks (441 us for 4 of
-//             1000 over 12000, 374 with bf16 pages).
+//             Their instructions are what bounds 8-bit chunks (435 us for 4 of
+//             1000 over 12000, 372 with bf16 pages).
 // TMEM (512 columns): two S buffers of 64 keys for each row tile, then O0 and
 // O1.  A key tile is taken in two steps of 64 keys, so that S of the next step
 // is computed while the softmax of this one runs: with one 128-key S per row
@@ -39,6 +39,7 @@
 // clock (64-key Q K^T: 48 KB in 256 clocks of products).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -840,37 +841,48 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const uint8_t *src = sst + st.slot * kStage + r0 * 128 + c16 * 16;
                     uint8_t *dst = skv + kv.slot * TILE;
                     // rows that are not there keep finite leftovers: their probabilities are exactly 0
-                    // four rows' codes are read before the first of them is stored: the
-                    // compiler cannot move a read over a store to the same memory
-                    uint2 u[4], v[4];
-                    uint32_t scales[4];
+                    uint32_t scales[8], top = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if ((i & 3) == 0)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                u[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + first * 8);
-                                v[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + 8 - first * 8);
-                                scales[k] = bars->scale[st.slot][r0 + 16 * (i + k)];
-                            }
-                        const uint32_t sb = scales[i & 3];
-                        const uint32_t w[4] = {u[i & 3].x, u[i & 3].y, v[i & 3].x, v[i & 3].y};
-                        uint32_t o[8];
-                        // 2^(120 + byte - 127) as a bf16 pair, up to 2^127
-                        uint32_t f = min(sb, 134u) * 0x00800080u + 0x3c003c00u;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny<0x9180>(w[q]), f);
-                            o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny<0xb3a2>(w[q]), f);
-                        }
-                        if (sb > 134u) {       // the rest of a scale above 2^7, or a row of NaN
-                            f = sb == 255u ? 0x7fff7fffu : (sb - 134u) * 0x00800080u + 0x3f803f80u;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) o[q] = bf16x2_mul(o[q], f);
-                        }
-                        *reinterpret_cast<uint4 *>(dst + at0 + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(dst + at1 + i * 2048) = make_uint4(o[4], o[5], o[6], o[7]);
+                        scales[i] = bars->scale[st.slot][r0 + 16 * i];
+                        top = max(top, scales[i]);
                     }
+                    // Four rows' codes are read before the first of them is stored (571 to 508 us
+                    // for 4 chunks of 1000 over 12000 cached; two 522, eight 540), and no
+                    // branch lies between rows (446 to 435): the compiler moves neither a read
+                    // over a store to the same memory nor anything over a branch.
+                    auto widen = [&](auto large) {
+                        uint2 u[4], v[4];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if ((i & 3) == 0)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    u[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + first * 8);
+                                    v[k] = *reinterpret_cast<const uint2 *>(src + (i + k) * 2048 + 8 - first * 8);
+                                }
+                            const uint32_t w[4] = {u[i & 3].x, u[i & 3].y, v[i & 3].x, v[i & 3].y};
+                            const uint32_t sb = scales[i];
+                            uint32_t o[8];
+                            // 2^(120 + byte - 127) as a bf16 pair, up to 2^127
+                            const uint32_t f = (large ? min(sb, 134u) : sb) * 0x00800080u + 0x3c003c00u;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                o[2 * q] = bf16x2_mul(e4m3_to_bf16_tiny<0x9180>(w[q]), f);
+                                o[2 * q + 1] = bf16x2_mul(e4m3_to_bf16_tiny<0xb3a2>(w[q]), f);
+                            }
+                            if (large) {           // the rest of a scale above 2^7, or a row of NaN
+                                const uint32_t g =
+                                    sb == 255u ? 0x7fff7fffu : (max(sb, 134u) - 134u) * 0x00800080u + 0x3f803f80u;
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) o[q] = bf16x2_mul(o[q], g);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + at0 + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + at1 + i * 2048) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    };
+                    if (__any_sync(0xffffffffu, top > 134u)) widen(std::true_type{});
+                    else widen(std::false_type{});
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(&bars->kv_full[kv.slot]));
                     mbar_arrive(smem_u32(&bars->st_empty[st.slot]));
@@ -1283,8 +1295,8 @@ constexpr int kSms = 148;
 // Rows (new tokens x group) a sequence up to which the warp-MMA kernel runs.
 // Measured with 32 / 8 heads, 16 caches of 8192, 64 of 2048 (us; 8, 16, 32, 64
 // rows): bf16 82, 84, 110, 215 against 111 of the tcgen05 kernel, and 83, 87,
-// 138, 210 against 127; 8-bit 53, 70, 130, 255 against 157, and 70, 99, 147,
-// 232 against 186.
+// 138, 210 against 127; 8-bit 53, 70, 130, 255 against 152, and 70, 99, 147,
+// 232 against 174.
 constexpr int kFewRows16 = 16, kFewRows8 = 32;
 constexpr int kFewRowsCtas16 = 2, kFewRowsCtas8 = 3;   // CTAs of that kernel an SM holds (bf16, 8-bit caches)
 constexpr int kFewRowsFixed = 16;          // what a piece costs besides its keys, in 16-key blocks
