@@ -342,7 +342,7 @@ size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int 
  *   lse[h,t] = ln sum_{s <= j <= t} exp(scale * q[t,h].k[j,h/G])
  * out [T][Hq][d] bf16 and lse [Hq][T] float, contiguous.  scale <= 0 selects
  * 1/sqrt(d).  max_len: the longest sequence (0: T); a longer one is recorded
- * as HS_ERR_INVALID_ARG and some of its rows are left out.  Rows of no
+ * as HS_ERR_INVALID_ARG and its rows' results are undefined.  Rows of no
  * sequence are left as they were.  Probabilities are rounded to bf16 before
  * they meet v; sums are held in fp32.  A score that is NaN or +infinity makes
  * its row's out and lse NaN.  A NaN or infinity in v[j] reaches that column
