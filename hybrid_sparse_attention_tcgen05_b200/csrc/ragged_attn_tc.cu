@@ -37,6 +37,9 @@
 // buffer and is the MMA's A operand there: P in shared memory would add its
 // writes and reads to an operand traffic that already fills the 128 bytes a
 // clock (64-key Q K^T: 48 KB in 256 clocks of products).
+// Bound: the softmax's chain of load, maximum, exponentials and store, with two
+// warps a scheduler: ~4000 clocks a pair of tiles against 2476 of products at
+// this step (8192-token prompt, 64/4 heads: 960 us, 1145 TFLOP/s).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
