@@ -97,6 +97,7 @@ struct RaggedBars {
     uint64_t pv_done[2];                  // each step's P V
     uint64_t o_full[2], o_empty[2];       // an item's last P V; O read out
     uint64_t work_full[2], work_empty[2];
+    uint64_t q_read;                      // solo: issuer 0's last product with the shared Q tile is done
     uint64_t side_full;                   // solo: warpgroup 1's half is in shared memory
     uint64_t drain[2];
     uint32_t tmem_base;
@@ -517,6 +518,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             mbar_init(smem_u32(&bars->work_full[w]), 1);
             mbar_init(smem_u32(&bars->work_empty[w]), readers);
         }
+        mbar_init(smem_u32(&bars->q_read), 1);
         mbar_init(smem_u32(&bars->side_full), 128);
         mbar_init(smem_u32(&bars->drain[0]), 1);
         mbar_init(smem_u32(&bars->drain[1]), 1);
@@ -775,7 +777,13 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         release(slot, true);
                     }
                 }
-                if (nw <= 1) commit_one(smem_u32(&bars->q_empty), leader);       // the last product with Q
+                // after the last product with Q; warpgroup 1 waits for issuer 0's before it
+                // stores its half of a joined item there
+                auto release_q = [&]() {
+                    commit_one(smem_u32(&bars->q_empty), leader);
+                    if (solo && w == 0 && n > 1) commit_one(smem_u32(&bars->q_read), leader);
+                };
+                if (nw <= 1) release_q();
                 // O may be overwritten once the item that had it before has been read out
                 if (nw > 0 && !wait(&bars->o_empty[w], o_free.take_free())) break;
                 int done = 0;                          // key tiles of this row tile
@@ -806,7 +814,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                             }
                         }
                         if (!ok) break;
-                        if (done + 1 == nw) commit_one(smem_u32(&bars->q_empty), leader);
+                        if (done + 1 == nw) release_q();
                     }
                     release(v, solo);
                     if (k_there) {
@@ -1042,14 +1050,18 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             float *const side = reinterpret_cast<float *>(sq) + tw * 128;   // 64 KB: the Q tiles, no longer read
             float a0 = 1.f, a1 = 0.f;
             if (join) {
-                // warpgroup 1 hands its half of the keys over through shared memory
+                // Warpgroup 1 hands its half of the keys over through shared memory, once
+                // issuer 0's products have read Q there: its last key tile may be the
+                // item's last, and then nothing else says that they have.
                 if (w == 1) {
+                    ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(&bars->q_read), side_phase.take(), p.wait_ns, abort));
+                    fin = ok;
                     bars->side[tw] = make_float2(fin ? m : nan, l);
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
                         load_o(c, o);
-                        if (valid) {
+                        if (valid && ok) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 *reinterpret_cast<float4 *>(side + (((8 * c + e) ^ (tw & 31)) << 2)) =
