@@ -627,9 +627,21 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const uint32_t dst = smem_u32(F8 ? sst + pos.slot * kStage : skv + pos.slot * TILE);
                     const CUtensorMap *m = is_v ? &tv : &tk;
                     const int bad = (k_tiles + j) % kBadBufs;
-                    if (!is_v) {
+                    if (!is_v && p.paged) {
+                        // Which keys lie on pages outside the pool, for the softmax to leave
+                        // out.  Written before the barrier's arrival below, which is what
+                        // the readers are ordered behind: the copies' bytes order nothing.
                         if (lane == 0) bars->bad_any[bad] = 0;
                         if (lane < 4) bars->bad[bad][lane] = 0;
+                        __syncwarp();
+                        for (int i = lane; i < boxes; i += 32) {
+                            const int pg = i < 32 ? page : __ldg(table + ((key0 + (i << rshift)) >> p.c.page_shift));
+                            if (pg >= 0 && pg < p.c.num_pages) continue;
+                            bars->bad_any[bad] = 1;
+                            for (int r = i << rshift; r < (i + 1) << rshift; ++r)
+                                atomicOr(&bars->bad[bad][r >> 5], 1u << (r & 31));
+                        }
+                        __syncwarp();
                     }
                     if (lane == 0) mbar_expect_tx(fb, (uint32_t)(boxes * p.box_rows * parts * row_bytes));
                     __syncwarp();
@@ -641,15 +653,9 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                             c2 = key & ((1 << p.c.page_shift) - 1);
                             c3 = page;
                             if (page < 0 || page >= p.c.num_pages) {
-                                // outside the pool: a box past the map's end reads zeros,
-                                // and the softmax leaves its keys out
+                                // outside the pool: a box past the map's end reads zeros
                                 report(p.status, HS_ERR_INVALID_INDEX);
                                 c3 = p.c.num_pages;
-                                if (!is_v) {
-                                    bars->bad_any[bad] = 1;
-                                    for (int r = i << rshift; r < (i + 1) << rshift; ++r)
-                                        atomicOr(&bars->bad[bad][r >> 5], 1u << (r & 31));
-                                }
                             }
                         }
                         for (int hf = 0; hf < parts; ++hf)
