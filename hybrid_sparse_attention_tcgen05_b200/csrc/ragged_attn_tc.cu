@@ -421,24 +421,27 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
     return r;
 }
 
-// 2^x for two x up to 8 (2^-126 below -126 and for NaN): 2^n by the exponent field, n = rint(x),
-// times a polynomial for the rest in [-0.5, 0.5] (degree 4, minimax in
-// relative error by the exchange algorithm: 2.6e-6, 1/1500 of a bf16
-// rounding, and 1.4e-8 on average, so sums of many keep fp32's accuracy).  It
-// runs on the FMA pipes beside the special-function unit, which at 16
+// 2^x for two x up to 8 (0 for x <= -127 and for NaN, less than 2^-126 between
+// -127 and -126.5): 2^n by the exponent field, n = rint(x), times a polynomial
+// for the rest in [-0.5, 0.5].  Degree 4, 1 at 0, the least largest
+// relative error with a mean of 0 (a linear programme over its coefficients):
+// 3.1e-6, 1/1270 of a bf16 rounding, and 6e-10 on average, so sums of many keep
+// fp32's accuracy.  That it is exactly 1 at 0 makes the result at -127, where
+// the exponent field gets to 0, exactly 0: a masked key's (-inf).
+// It runs on the FMA pipes beside the special-function unit, which at 16
 // results a clock would otherwise bound the softmax (128 x 128 x 2 per 2048
 // clocks of products).
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
     const float magic = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer, left in the low bits
-    x.x = fmaxf(x.x, -126.f);
-    x.y = fmaxf(x.y, -126.f);
+    x.x = fmaxf(x.x, -127.f);
+    x.y = fmaxf(x.y, -127.f);
     const float2 t = fadd2(x, make_float2(magic, magic));
     const float2 r = fadd2(t, make_float2(-magic, -magic));
     const float2 f = ffma2(r, make_float2(-1.f, -1.f), x);
-    float2 y = ffma2(f, make_float2(0.00957010191f, 0.00957010191f), make_float2(0.0559178603f, 0.0559178603f));
-    y = ffma2(y, f, make_float2(0.240247448f, 0.240247448f));
-    y = ffma2(y, f, make_float2(0.693121815f, 0.693121815f));
-    y = ffma2(y, f, make_float2(0.999999261f, 0.999999261f));
+    float2 y = ffma2(f, make_float2(0.00962985866f, 0.00962985866f), make_float2(0.0559173897f, 0.0559173897f));
+    y = ffma2(y, f, make_float2(0.240228951f, 0.240228951f));
+    y = ffma2(y, f, make_float2(0.693121016f, 0.693121016f));
+    y = ffma2(y, f, make_float2(1.f, 1.f));
     return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
                        __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
 }
@@ -1007,8 +1010,7 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     }
                     m = m_new;
                 }
-                // masked keys (-inf) give 0, or 2^-126 by exp2_fma, which beside a seen
-                // key's is nothing; a row that has seen none is set right at the end
+                // masked keys (-inf) give exactly 0
                 const float mref = m == -INFINITY ? 0.f : m;
                 const float2 c2v = make_float2(c2, c2), mv = make_float2(-mref, -mref);
                 float2 ps01 = make_float2(0.f, 0.f), ps23 = make_float2(0.f, 0.f);
@@ -1041,7 +1043,6 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             if (nw > 0)
                 ok = __all_sync(0xffffffffu, ok && bar_wait(smem_u32(&bars->o_full[w]), o_phase.take(), p.wait_ns, abort));
             bool fin = ok;
-            if (m == -INFINITY) l = 0.f;               // nothing seen
             tc_fence_after();
             // O of this thread's row: columns [32 c, 32 c + 32), zeros when there were no tiles
             auto load_o = [&](int c, float (&o)[32]) {

@@ -37,3 +37,72 @@ def test_every_third_page_outside_the_pool(P, pool):
         first = first or (out.clone(), lse.clone())
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     _check_all(f"P {P}", q, got, cu, new, out, lse, dropped=dropped)
+
+
+HUGE = 1e38
+
+
+@pytest.mark.parametrize("new,old", [([200, 90], [0, 0]), ([140, 20], [300, 700]), ([20, 3], [2000, 900]), ([4, 2], [500, 31])])
+@pytest.mark.parametrize("pool", ["packed", "bf16", "e4m3"])
+def test_huge_values_behind_a_row_do_not_reach_it(pool, new, old):
+    """Finite values near the type's largest at positions that a row does not see: its result is the
+    definition's, wherever in a tile they lie.  (Rows that do see one are not looked at: their sums in
+    fp32 may overflow before the division.)"""
+    gen = torch.Generator().manual_seed(sum(new) + len(pool))
+    if pool == "packed":
+        old = [0, 0]
+    hq, hkv, P = 8, 2, 16
+    kv, cu, T = [a + b for a, b in zip(new, old)], ref.cu_of(new), sum(new)
+    q = torch.randn(T, hq, 128, generator=gen).to(BF)
+    k, v = (torch.randn(sum(kv), hkv, 128, generator=gen).to(BF) for _ in range(2))
+    at = [range(m - n + 1, m) for n, m in zip(new, kv)]          # all but the first new row
+    first = ref.cu_of(kv)
+    table, pages = ref.make_table(gen, [-(-m // P) for m in kv])
+    dt = table.to(DEV)
+    sc = {}
+    if pool == "e4m3":
+        sc = {n: torch.zeros(pages, hkv, P, dtype=torch.uint8, device=DEV) for n in ("k_scale", "v_scale")}
+    dtype = torch.float8_e4m3fn if pool == "e4m3" else BF
+    pk, pv = (torch.zeros(pages, P, hkv, 128, device=DEV).to(dtype) for _ in range(2))
+    for step in (1, 3, 16, 37):                                  # huge from a row on: every step-th new position
+        vx = v.clone()
+        lim = []
+        for b in range(2):
+            hit = list(at[b])[step - 1::step][:40]
+            for i, j in enumerate(hit):
+                vx[int(first[b]) + j] = HUGE * (-1) ** i
+            lim.append(min(hit) - (kv[b] - new[b]) if hit else new[b])     # new rows that see none of them
+        if pool == "packed":
+            out, lse = hs.packed_attn(q.to(DEV), k.to(DEV), vx.to(DEV), cu.to(DEV), max_len=max(new))
+            rk, rv = k, vx
+        else:
+            hs.cache_write(k.to(DEV), vx.to(DEV), pk, pv, first.to(DEV), _int(kv), dt, **sc)
+            out, lse = hs.chunk_attn_paged(q.to(DEV), pk, pv, cu.to(DEV), _int(kv), dt, max_q=max(new), max_len=max(kv), **sc)
+            rk, rv = (x.cpu() for x in hs.cache_read(pk, pv, first.to(DEV), dt, total=sum(kv), dtype=torch.float32, **sc))
+        for b in range(2):
+            r0, n = int(cu[b]), lim[b]
+            rows = slice(int(first[b]), int(first[b]) + kv[b] - new[b] + n)
+            ref.check_attend(f"step {step} seq {b}", out[r0:r0 + n], lse[:, r0:r0 + n],
+                             ref.attend(q[r0:r0 + n], rk[rows], rv[rows], SCALE))
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_keys_far_below_the_maximum_give_nothing(new):
+    """Probabilities below the smallest float are 0, also beside huge values."""
+    gen = torch.Generator().manual_seed(new)
+    hq, hkv, m = 8, 2, 300
+    e = torch.where(torch.rand(128, generator=gen) < 0.5, -1.0, 1.0)
+    for rows in (new, 90):
+        q = (0.1 * torch.randn(rows, hq, 128, generator=gen) + e).to(BF)
+        k = 0.1 * torch.randn(m, hkv, 128, generator=gen)
+        v = torch.randn(m, hkv, 128, generator=gen)
+        low = torch.arange(m) % 5 != 0
+        k[low] -= 20.0 * e                    # 20 * 128 / sqrt(128) = 226 below, in natural units
+        v[low] = HUGE
+        k, v = k.to(BF), v.to(BF)
+        table = _int([list(range(5))])
+        pk, pv = (torch.zeros(5, 64, hkv, 128, dtype=BF, device=DEV) for _ in range(2))
+        hs.cache_write(k.to(DEV), v.to(DEV), pk, pv, _int([0, m]), _int([m]), table)
+        out, lse = hs.chunk_attn_paged(q.to(DEV), pk, pv, _int([0, rows]), _int([m]), table, max_q=rows, max_len=m)
+        # scores of up to 226: 128 * 2^-24 * 226 * 2
+        ref.check_attend(f"{rows} rows", out, lse, ref.attend(q, k, v, SCALE), slack=4e-3)
