@@ -23,9 +23,11 @@
 // 8-bit caches: a code widens to fp16 exactly (one conversion per two codes)
 // and the MMAs run in fp16.  The rows' scales stay out of the operands: the
 // key's power of two joins the score, the value's joins the probability, whose
-// running reference is the largest probability x scale, so that it neither
-// overflows fp16 nor loses bits; the sum of probabilities keeps a reference
-// of its own.  Queries are scaled to [1, 2) by a power of two per row, which
+// running reference is 2^-7 of the largest probability x scale among rows that
+// are not all zeros (a row of zeros has whatever scale its writer gave it), so
+// that products stay below 2^15 and lose bits only from 2^-21 of the largest
+// down: each is off by 2^-11 of itself or 2^-32 of the largest.  The sum of
+// probabilities keeps a reference of its own.  Queries are scaled to [1, 2) by a power of two per row, which
 // makes their fp16 form exact for elements within 2^-14 of the row's largest
 // (2^-25 of that element's size below).  fp16 probabilities are rounded by
 // 2^-11; for bf16 caches they are rounded to bf16 (2^-8), the type of V.
@@ -49,6 +51,11 @@ constexpr int kBlock = 16;         // keys a warp takes at a time
 // Reference of a row that has seen no key: finite, so that differences with
 // it need no special case, and below every score but the last float's.
 constexpr float kNone = -3.4e38f;
+// How far below a row's maximum (log2 units) a new reference is put, and how
+// far above it a score may rise before it moves.
+template <bool F8> struct Ref {
+    static constexpr float below = F8 ? 7.f : 0.f, above = F8 ? 15.f : 8.f;
+};
 
 template <bool F8> struct Cfg {
     static constexpr int row = F8 ? 128 : 256;                     // bytes of a K or V row
@@ -381,12 +388,30 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
                 for (int e = 0; e < 2; ++e) y[t][2 * k + e] = F8 ? x[t][2 * k + e] + ev[k] : x[t][2 * k + e];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                grow = grow || fmaxf(y[t][e], y[t][2 + e]) > my[t][e] + 8.f;
+                grow = grow || fmaxf(y[t][e], y[t][2 + e]) > my[t][e] + Ref<F8>::above;
                 if (F8) grow = grow || fmaxf(x[t][e], x[t][2 + e]) > mx[t][e] + 8.f;
             }
         }
         // the references move only when a row's maximum grows by more than 8
         if (__any_sync(0xffffffffu, grow)) {
+            if (F8) {
+                // value rows of zeros give nothing: their scales move no reference
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 *vr = reinterpret_cast<const uint4 *>(blk + (kBlock + gl + 8 * k) * C::row + 32 * c);
+                    const uint4 u = vr[0], w = vr[1];
+                    uint32_t any = (u.x | u.y | u.z | u.w | w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+                    any |= __shfl_xor_sync(0xffffffffu, any, 1);
+                    any |= __shfl_xor_sync(0xffffffffu, any, 2);
+                    if (any == 0) {                  // (NaN and infinity stay: they make the row NaN)
+#pragma unroll
+                        for (int t = 0; t < NB; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (y[t][2 * k + e] < INFINITY) y[t][2 * k + e] = -INFINITY;
+                    }
+                }
+            }
 #pragma unroll
             for (int t = 0; t < NB; ++t)
 #pragma unroll
@@ -398,7 +423,7 @@ __global__ void __launch_bounds__(32 * kWarps, F8 ? 3 : 2) ragged_rows(const Par
                         if (F8) tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, d));
                     }
                     if (!F8) tx = ty;
-                    const float ny = fmaxf(my[t][e], ty), nx = fmaxf(mx[t][e], tx);
+                    const float ny = fmaxf(my[t][e], ty - Ref<F8>::below), nx = fmaxf(mx[t][e], tx);
                     const float cy = ex2(my[t][e] - ny);
                     l[t][e] *= ex2(mx[t][e] - nx);
                     my[t][e] = ny;

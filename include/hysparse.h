@@ -366,7 +366,10 @@ int hysparse_packed_attn(const int32_t *cu_rows, int B, int T, int Hq, int Hkv, 
  * as in hysparse_packed_attn; a row that sees nothing (kv_len[b] < n) gets
  * zeros and lse = -inf.  max_len: the longest cache (0: max_pages *
  * page_size); it only plans the work, longer ones are still right.
- * Pools of HS_BF16 or HS_E4M3.  Only the table entries that cover
+ * Pools of HS_BF16 or HS_E4M3.  Few rows a sequence over HS_E4M3: each product
+ * of a probability and its value row's scale is off by 2^-11 of itself or 2^-32
+ * of the row's largest such product (rows of zeros left out), whichever is more.
+ * Only the table entries that cover
  * positions 0 .. kv_len[b]-1 are read, and nothing that lies behind
  * kv_len[b] in the last page reaches a result (NaN included).  A page outside
  * the pool drops its keys.  ws: 256-byte aligned,

@@ -106,3 +106,26 @@ def test_keys_far_below_the_maximum_give_nothing(new):
         out, lse = hs.chunk_attn_paged(q.to(DEV), pk, pv, _int([0, rows]), _int([m]), table, max_q=rows, max_len=m)
         # scores of up to 226: 128 * 2^-24 * 226 * 2
         ref.check_attend(f"{rows} rows", out, lse, ref.attend(q, k, v, SCALE), slack=4e-3)
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-6, 1e-12])
+@pytest.mark.parametrize("new", [1, 4, 40])
+def test_8bit_rows_of_zeros_beside_small_values(new, size):
+    """A value row of zeros has the scale 2^0; where its key has the largest score, small values beside
+    it keep their bits."""
+    gen = torch.Generator().manual_seed(new)
+    hq, hkv, P, m = 8, 2, 16, 200
+    q = torch.randn(new, hq, 128, generator=gen).to(BF)
+    k, v = torch.randn(m, hkv, 128, generator=gen), torch.randn(m, hkv, 128, generator=gen) * size
+    v[::7] = 0
+    v[3::7] = -0.0
+    k[5] = 1.5 * q.float().view(new, hkv, hq // hkv, 128)[0].mean(1)      # above the others for the first row
+    v[5] = 0
+    table = _int([list(range(13))])
+    pk, pv = (torch.zeros(13, P, hkv, 128, device=DEV).to(torch.float8_e4m3fn) for _ in range(2))
+    sc = {n: torch.zeros(13, hkv, P, dtype=torch.uint8, device=DEV) for n in ("k_scale", "v_scale")}
+    hs.cache_write(k.to(DEV), v.to(DEV), pk, pv, _int([0, m]), _int([m]), table, **sc)
+    assert bool((sc["v_scale"][0, :, 5] == 127).all())
+    rk, rv = (x.cpu() for x in hs.cache_read(pk, pv, _int([0, m]), table, total=m, dtype=torch.float32, **sc))
+    out, lse = hs.chunk_attn_paged(q.to(DEV), pk, pv, _int([0, new]), _int([m]), table, max_q=new, max_len=m, **sc)
+    ref.check_attend(f"{new} rows", out, lse, ref.attend(q, rk, rv, SCALE))
