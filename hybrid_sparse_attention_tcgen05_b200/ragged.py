@@ -59,7 +59,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: Optional[s
       slowest pair is slowed by factor, the fastest not at all.
     * "parts"    -- by the turns a pair makes over original_len positions: pairs
       with at least ``fast`` turns stay, pairs with at most ``slow`` are divided
-      by factor, those between are mixed linearly in the pair's index; the
+      by factor, those between are mixed linearly in the pair's index (the two
+      ends rounded outwards to whole indices, within 0 and rot_dim - 1); the
       amplitude is 0.1 ln(factor) + 1.
     * "bands"    -- as "parts", but mixed linearly in the number of turns and
       with amplitude 1.
@@ -89,7 +90,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: Optional[s
             def index_of(t):
                 return rot_dim * math.log(original_len / (t * 2 * math.pi)) / (2 * math.log(base))
 
-            lo, hi = max(math.floor(index_of(fast)), 0), min(math.ceil(index_of(slow)), half - 1)
+            # hi may lie beyond the last pair, which then makes more than `slow` turns
+            lo, hi = max(math.floor(index_of(fast)), 0), min(math.ceil(index_of(slow)), rot_dim - 1)
             keep = 1.0 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
             amp = 0.1 * math.log(factor) + 1.0
         freq = freq * keep + freq / factor * (1.0 - keep)

@@ -160,3 +160,29 @@ def test_binding_shares_the_cpp_runtime(L):
     import subprocess
     needs = subprocess.run(["ldd", hs_build.BINDING], capture_output=True, text=True, check=True).stdout
     assert "libstdc++" in needs
+
+
+@pytest.mark.parametrize("rot,base,length,factor", [(128, 1e4, 131072, 4.0), (128, 1e4, 65536, 4.0), (64, 1e4, 1 << 20, 8.0),
+                                                    (128, 1e4, 32768, 4.0), (128, 5e5, 131072, 8.0), (64, 1e4, 8192, 4.0)])
+def test_rope_frequencies_parts_ramp(rot, base, length, factor):
+    """The ramp from kept to divided pairs is linear in the pair's index between the indices that make 32
+    turns and one turn over the trained length (rounded outwards), also where the latter lies
+    beyond the last pair: that pair, which makes more than one turn, is then not divided wholly."""
+    import math
+
+    import hybrid_sparse_attention_tcgen05_b200 as hs
+    f, amp = hs.rope_frequencies(rot, base, scaling="parts", factor=factor, original_len=length, device="cpu")
+
+    def index(turns):            # the pair whose angle makes that many turns: base^(-2 i / rot) length = 2 pi turns
+        return rot / 2 * math.log(length / (2 * math.pi * turns), base)
+    lo, hi = max(math.floor(index(32)), 0), min(math.ceil(index(1)), rot - 1)
+    for i in range(rot // 2):
+        plain = base ** (-2 * i / rot)
+        mix = min(max((i - lo) / (hi - lo), 0), 1)                # 0: kept, 1: divided
+        assert abs(float(f[i]) / (plain * (1 - mix) + plain / factor * mix) - 1) < 1e-12, i
+        turns = length * plain / (2 * math.pi)
+        if i < lo:
+            assert float(f[i]) == plain
+        if turns > 1:
+            assert float(f[i]) > plain / factor, i
+    assert abs(amp - (0.1 * math.log(factor) + 1)) < 1e-15
