@@ -129,3 +129,36 @@ def test_8bit_rows_of_zeros_beside_small_values(new, size):
     rk, rv = (x.cpu() for x in hs.cache_read(pk, pv, _int([0, m]), table, total=m, dtype=torch.float32, **sc))
     out, lse = hs.chunk_attn_paged(q.to(DEV), pk, pv, _int([0, new]), _int([m]), table, max_q=new, max_len=m, **sc)
     ref.check_attend(f"{new} rows", out, lse, ref.attend(q, rk, rv, SCALE))
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (6, 2), (7, 1)])
+@pytest.mark.parametrize("fill", [math.nan, 3e38, 0.0])
+def test_rows_of_others_in_a_tile_change_nothing(hq, hkv, fill):
+    """Whatever lies in a row tile beside a sequence's own rows, its rows are the same bits: rows of nobody
+    between sequences that hold NaN, huge numbers or zeros, and group sizes that do not fill a tile."""
+    gen = torch.Generator().manual_seed(hq)
+    lens, gap, T = [70, 5, 33, 130], 40, 4 * 170
+    q, k, v = (torch.randn(T, h, 128, generator=gen).to(BF) for h in (hq, hkv, hkv))
+    # every second sequence has no keys and is the gap behind the one before it; its rows hold `fill`
+    cu, kv, at = [], [], 0
+    for n in lens:
+        cu += [at, at + n]
+        kv += [n + 600, 0]
+        at += n + gap
+    cu.append(at)
+    table, got = _paged(gen, kv, 32, hkv, "bf16")
+    plain = q.clone()
+    for i in range(len(lens)):
+        q[cu[2 * i + 1]:cu[2 * i + 2]] = fill
+    dcu = _int(cu)
+    first = None
+    for x in (plain, q):
+        out, lse = hs.chunk_attn_paged(x.to(DEV), got["k"][0], got["v"][0], dcu, _int(kv), table.to(DEV), max_q=130,
+                                       max_len=max(kv))
+        rows = torch.cat([torch.arange(cu[2 * i], cu[2 * i + 1]) for i in range(len(lens))]).to(DEV)
+        first = first or (out[rows], lse[:, rows])
+        assert torch.equal(out[rows], first[0]) and torch.equal(lse[:, rows], first[1])
+    for i, n in enumerate(lens):
+        part = slice(cu[2 * i], cu[2 * i] + n)
+        ref.check_attend(f"seq {i}", out[part], lse[:, part],
+                         ref.attend(plain[part], got["k"][2][2 * i], got["v"][2][2 * i], SCALE))
