@@ -98,8 +98,6 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
         if force or ptxas_verbose or not os.path.exists(obj) or \
                 os.path.getmtime(obj) < max(os.path.getmtime(src), dep_t):
             jobs.append((src, obj))
-    if force or _binding_stale():
-        _build_binding()
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
             futs = {ex.submit(_compile, s, o, ptxas_verbose): s for s, o in jobs}
@@ -115,6 +113,9 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB)
+    # last: it needs torch's and Python's headers, which callers of the C library may lack
+    if force or _binding_stale():
+        _build_binding()
     return LIB
 
 

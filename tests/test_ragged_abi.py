@@ -186,3 +186,17 @@ def test_rope_frequencies_parts_ramp(rot, base, length, factor):
         if turns > 1:
             assert float(f[i]) > plain / factor, i
     assert abs(amp - (0.1 * math.log(factor) + 1)) < 1e-15
+
+
+def test_library_is_built_where_the_binding_cannot_be(L, monkeypatch, tmp_path):
+    """The C library needs nvcc only: without the headers of torch and Python it is built all the same,
+    and then the binding's failure is raised."""
+    def no_headers():
+        raise RuntimeError("no headers")
+    lib = tmp_path / "libhysparse.so"
+    monkeypatch.setattr(hs_build, "LIB", str(lib))
+    monkeypatch.setattr(hs_build, "_binding_stale", lambda: True)
+    monkeypatch.setattr(hs_build, "_build_binding", no_headers)
+    with pytest.raises(RuntimeError, match="no headers"):
+        hs_build.build()
+    assert ctypes.CDLL(str(lib)).hysparse_version is not None
