@@ -49,6 +49,11 @@ double number(PyObject *o) {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return v;
 }
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v != 0;
+}
 int as_int(int64_t v, const char *what) {
     TORCH_CHECK_VALUE(v >= INT_MIN && v <= INT_MAX, what, " is out of range");
     return (int)v;
@@ -196,7 +201,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     need_args(n, 9);
     const at::Tensor q = tensor(a[0], "q"), positions = tensor(a[1], "positions"), f = tensor(a[2], "inv_freq");
     const at::Tensor k = maybe_tensor(a[3], "k");
-    const int flags = (PyObject_IsTrue(a[4]) ? HS_ROPE_INTERLEAVED : 0) | (PyObject_IsTrue(a[5]) ? HS_ROPE_INVERSE : 0);
+    const int flags = (truth(a[4]) ? HS_ROPE_INTERLEAVED : 0) | (truth(a[5]) ? HS_ROPE_INVERSE : 0);
     const float factor = (float)number(a[6]);
     at::Tensor out = maybe_tensor(a[7], "out"), out_k = maybe_tensor(a[8], "out_k");
     Device dev(q, positions, f, k, out, out_k);
@@ -233,7 +238,7 @@ PyObject *cache_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor k = tensor(a[0], "k"), v = tensor(a[1], "v"), kp = tensor(a[2], "k_pages"), vp = tensor(a[3], "v_pages");
     const at::Tensor cu = tensor(a[4], "cu_seqlens"), kv = tensor(a[5], "kv_len"), table = tensor(a[6], "block_table");
     const at::Tensor ks = maybe_tensor(a[7], "k_scale"), vs = maybe_tensor(a[8], "v_scale"), f = maybe_tensor(a[9], "inv_freq");
-    const int flags = PyObject_IsTrue(a[10]) ? HS_ROPE_INTERLEAVED : 0;
+    const int flags = truth(a[10]) ? HS_ROPE_INTERLEAVED : 0;
     const float factor = (float)number(a[11]);
     const at::Tensor ws = maybe_tensor(a[12], "ws");
     Device dev(k, v, kp, vp, cu, kv, table, ks, vs, f, ws);
@@ -261,7 +266,7 @@ PyObject *cache_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int total = as_int(integer(a[4]), "total");
     TORCH_CHECK_VALUE(total >= 0, "total must not be negative");
     const at::Tensor start = maybe_tensor(a[5], "start"), ks = maybe_tensor(a[6], "k_scale"), vs = maybe_tensor(a[7], "v_scale");
-    const at::ScalarType dtype = PyObject_IsTrue(a[8]) ? at::kBFloat16 : at::kFloat;
+    const at::ScalarType dtype = truth(a[8]) ? at::kBFloat16 : at::kFloat;
     at::Tensor ok = maybe_tensor(a[9], "out_k"), ov = maybe_tensor(a[10], "out_v");
     const at::Tensor ws = maybe_tensor(a[11], "ws");
     Device dev(kp, vp, cu, table, start, ks, vs, ok, ov, ws);

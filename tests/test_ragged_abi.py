@@ -200,3 +200,17 @@ def test_library_is_built_where_the_binding_cannot_be(L, monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="no headers"):
         hs_build.build()
     assert ctypes.CDLL(str(lib)).hysparse_version is not None
+
+
+def test_binding_raises_what_a_flag_raises():
+    """A flag that has no truth value is an error of its own, not a call with the flag set."""
+    import torch
+
+    import hybrid_sparse_attention_tcgen05_b200 as hs
+    both = torch.ones(2)
+    q, pos, f = torch.zeros(4, 2, 64), torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
+    pages = torch.zeros(2, 16, 2, 64)
+    for call in (lambda: hs.rope(q, pos, f, interleaved=both), lambda: hs.rope(q, pos, f, inverse=both),
+                 lambda: hs.cache_write(q, q, pages, pages, pos, pos, pos, interleaved=both)):
+        with pytest.raises(RuntimeError, match="Boolean value"):
+            call()
