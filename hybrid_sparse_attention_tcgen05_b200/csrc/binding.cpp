@@ -168,6 +168,16 @@ void status_ws(const at::Tensor &ws) {
                       "ws must be contiguous and hold at least 256 bytes");
 }
 
+// Marks the caller's tensors as changed, as torch's own writes do, so that a
+// backward pass that saved one of them raises instead of using what was written
+// over it.  (Tensors made in inference mode keep no count of changes.)
+template <typename... Ts> void changed(const Ts &...ts) {
+    auto mark = [](const at::Tensor &t) {
+        if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    };
+    (mark(ts), ...);
+}
+
 // Runs call(stream) on the device and its current stream, without the
 // interpreter's lock; false with the library's error raised.
 template <typename F>
@@ -227,6 +237,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return g_rope(rq.T, rq.H, rk.H, rq.d, code, ptr(q), rq.ld, ptr(k), rk.ld, (const int32_t *)ptr(positions),
                              (const double *)ptr(f), rot, flags, factor, mut(out), ro.ld, mut(out_k), rok.ld, st);
     })) return nullptr;
+    changed(out, out_k);
     return k.defined() ? pair(out, out_k) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -253,6 +264,7 @@ PyObject *cache_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return g_cache_write(&p.c, rk.T, rk.H, rk.d, code, ptr(k), rk.ld, ptr(v), rv.ld, (const double *)ptr(f), rot,
                                     flags, factor, mut(ws), st);
     })) return nullptr;
+    changed(kp, vp, ks, vs);
     return Py_NewRef(Py_None);
     END_HANDLE_TH_ERRORS
 }
@@ -282,6 +294,7 @@ PyObject *cache_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return g_cache_read(&p.c, (const int32_t *)ptr(start), total, p.Hkv, p.d, code_of(dtype), mut(ok), mut(ov),
                                    mut(ws), st);
     })) return nullptr;
+    changed(ok, ov);
     return pair(ok, ov);
     END_HANDLE_TH_ERRORS
 }
@@ -341,6 +354,7 @@ PyObject *packed_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                     ptr(k), rk.ld, ptr(v), rv.ld, mut(b.out), (float *)mut(b.lse), mut(b.ws), b.ws.nbytes(),
                                     st);
     })) return nullptr;
+    changed(b.out, b.lse);
     return pair(b.out, b.lse);
     END_HANDLE_TH_ERRORS
 }
@@ -364,6 +378,7 @@ PyObject *chunk_attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return g_chunk_attn(&p.c, b.q.T, b.q.H, p.Hkv, b.q.d, most, longest, scale, ptr(q), b.q.ld, mut(b.out),
                                          (float *)mut(b.lse), mut(b.ws), b.ws.nbytes(), st);
     })) return nullptr;
+    changed(b.out, b.lse);
     return pair(b.out, b.lse);
     END_HANDLE_TH_ERRORS
 }

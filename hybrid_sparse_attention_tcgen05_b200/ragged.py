@@ -7,6 +7,11 @@ work is the library's (include/hysparse.h, "Ragged batches and paged caches").
 Packed tensors are [T, H, d], the rows of all sequences one after the other;
 they may be slices of one projection's output (any stride between rows that
 is a multiple of 16 bytes).
+
+Nothing here is recorded for autograd: results carry no gradient, also where
+inputs require one (rope's is rope with ``inverse`` on the results' gradients).
+Tensors that a call writes into (out, pages, scales ...) count as changed, so a
+backward pass that saved one of them raises.
 """
 from __future__ import annotations
 
