@@ -332,7 +332,7 @@ AttnBuffers attn_buffers(const at::Tensor &q, int Hkv, int B, int max_q, int max
     return b;
 }
 
-// packed_attn(q, k, v, cu, max_len (< 0: T), scale, out, lse, ws)
+// packed_attn(q, k, v, cu, max_len (None or 0: T), scale, out, lse, ws)
 PyObject *packed_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     need_args(n, 9);
@@ -347,7 +347,8 @@ PyObject *packed_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(cu.dim() == 1 && cu.size(0) >= 2, "cu_seqlens must hold B + 1 entries");
     dense(cu, "cu_seqlens", at::kInt, {cu.size(0)});
     const int B = as_int(cu.size(0) - 1, "B");
-    const int longest = a[4] == Py_None ? rk.T : as_int(integer(a[4]), "max_len");
+    int longest = a[4] == Py_None ? 0 : as_int(integer(a[4]), "max_len");
+    if (longest == 0) longest = rk.T;
     const AttnBuffers b = attn_buffers(q, rk.H, B, longest, longest, a[6], a[7], a[8]);
     if (!run(dev, "hysparse_packed_attn", [&](hs_stream_t st) {
         return g_packed_attn((const int32_t *)ptr(cu), B, b.q.T, b.q.H, rk.H, b.q.d, longest, scale, ptr(q), b.q.ld,
@@ -372,7 +373,8 @@ PyObject *chunk_attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Pages p = pages_of(kp, vp, cu, kv, table, ks, vs);
     TORCH_CHECK_VALUE(q.dim() == 3 && q.size(2) == p.d, "q and the pages disagree on head dim");
     const int most = a[6] == Py_None ? as_int(q.size(0), "T") : as_int(integer(a[6]), "max_q");
-    const int longest = as_int(a[7] == Py_None ? (int64_t)p.c.max_pages * p.c.page_size : integer(a[7]), "max_len");
+    int longest = a[7] == Py_None ? 0 : as_int(integer(a[7]), "max_len");
+    if (longest == 0) longest = as_int((int64_t)p.c.max_pages * p.c.page_size, "max_pages * page_size");
     const AttnBuffers b = attn_buffers(q, p.Hkv, p.c.B, most, longest, a[11], a[12], a[13]);
     if (!run(dev, "hysparse_chunk_attn_paged", [&](hs_stream_t st) {
         return g_chunk_attn(&p.c, b.q.T, b.q.H, p.Hkv, b.q.d, most, longest, scale, ptr(q), b.q.ld, mut(b.out),

@@ -163,6 +163,7 @@ struct RaggedPlan {
     size_t ml_off = 0, o_off = 0, bytes = 0;
 };
 RaggedPlan ragged_plan(const RaggedCall &a);
+size_t ragged_most_bytes(const RaggedCall &a);
 // ragged_rows_mma.cu: at most pl.tile_rows x pl.tiles rows a sequence and KV head, paged
 cudaError_t ragged_rows_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, cudaStream_t st);
 cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, unsigned long long wait_ns,

@@ -172,6 +172,7 @@ int hysparse_cache_read(const hs_paged_cache *cache, const int32_t *start, int t
 size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int max_q, int max_len) {
     RaggedCall a{};
     if (resolve_attn(B, T, Hq, Hkv, d, max_q, max_len, 0.f, &a) != HS_OK) return 0;
+    if (max_len == 0) return ragged_most_bytes(a);
     size_t n = ragged_plan(a).bytes;   // whichever call and pool it is for
     for (int dtype : {(int)HS_BF16, (int)HS_E4M3}) {
         a.paged = true;

@@ -1431,6 +1431,16 @@ RaggedPlan ragged_plan(const RaggedCall &a) {
     return pl;
 }
 
+// No plan for these rows takes more, whatever the keys' lengths.
+size_t ragged_most_bytes(const RaggedCall &a) {
+    using namespace tc;
+    const size_t rows = (size_t)a.T * a.Hq;
+    RaggedPlan pl;
+    if (rows > 0) pl.splits = (int)std::max<size_t>(1, std::min<size_t>(kMaxSplits, kMaxPartRows / rows));
+    plan_bytes(rows, &pl);
+    return pl.bytes;
+}
+
 cudaError_t ragged_attn_launch(const RaggedCall &a, const RaggedPlan &pl, void *ws, unsigned long long wait_ns,
                                cudaStream_t st) {
     using namespace tc;

@@ -157,7 +157,9 @@ def cache_read(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_rows: torch.Tens
 
 def ragged_workspace_size(B: int, T: int, Hq: int, Hkv: int, d: int = 128, max_q: int = 0, max_len: int = 0) -> int:
     """Bytes of workspace of packed_attn (max_q = max_len = the longest prompt) and
-    chunk_attn_paged (most new rows of a sequence; the longest cache)."""
+    chunk_attn_paged (most new rows of a sequence; the longest cache; 0: any).
+    Fewer rows can need more than many, so a loop over batches of different
+    sizes keeps one workspace of the most there is, 94 << 20."""
     n = _lib.lib().hysparse_ragged_workspace_size(B, T, Hq, Hkv, d, max_q, max_len)
     if n == 0:
         raise _lib.HysparseError(_lib.HS_ERR_INVALID_ARG, "hysparse_ragged_workspace_size")

@@ -330,8 +330,11 @@ int hysparse_cache_read(const hs_paged_cache *cache, const int32_t *start, int t
 /* Bytes of workspace that the two attention calls below need for these
  * arguments (0 for invalid ones): 256 for the status word, and where few rows
  * face many keys, the partial results of the pieces their keys are split
- * into.  At most 94 MB.  A workspace belongs to one call at a time:
- * calls (or replayed graphs) that may overlap on the GPU need one each.
+ * into.  max_len 0: enough for any length.  At most 94 MB, which serve every
+ * call; fewer rows can need more than many (their keys are cut into more
+ * pieces), so a loop over batches of different sizes keeps one of 94 MB.
+ * A workspace belongs to one call at a time: calls (or replayed graphs) that
+ * may overlap on the GPU need one each.
  * Status word as in hysparse_workspace_size. */
 size_t hysparse_ragged_workspace_size(int B, int T, int Hq, int Hkv, int d, int max_q, int max_len);
 

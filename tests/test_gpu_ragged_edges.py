@@ -162,3 +162,23 @@ def test_rows_of_others_in_a_tile_change_nothing(hq, hkv, fill):
         part = slice(cu[2 * i], cu[2 * i] + n)
         ref.check_attend(f"seq {i}", out[part], lse[:, part],
                          ref.attend(plain[part], got["k"][2][2 * i], got["v"][2][2 * i], SCALE))
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_workspace_sized_without_lengths(T):
+    """The size for no stated lengths serves calls that state none."""
+    gen = torch.Generator().manual_seed(T)
+    hq, hkv, n = 4, 1, 6000
+    table, got = _paged(gen, [n], 64, hkv, "bf16")
+    q = torch.randn(T, hq, 128, generator=gen).to(BF)
+    ws = torch.zeros(hs.ragged_workspace_size(1, T, hq, hkv), dtype=torch.uint8, device=DEV)
+    for kw in (dict(), dict(max_len=0), dict(max_q=0, max_len=0)):
+        for w in (ws, None):
+            out, lse = _chunk(q, got, ref.cu_of([T]), [n], table, ws=w, **kw)
+            _check_all(str(kw), q, got, ref.cu_of([T]), [T], out, lse)
+    assert hs.workspace_status(ws) == _lib.HS_OK
+    k = torch.randn(T, hkv, 128, generator=gen).to(BF)
+    for kw in (dict(), dict(max_len=0)):
+        for w in (ws, None):
+            out, lse = hs.packed_attn(q.to(DEV), k.to(DEV), k.to(DEV), _int([0, T]), ws=w, **kw)
+            ref.check_attend(str(kw), out, lse, ref.attend(q, k, k, SCALE))

@@ -214,3 +214,14 @@ def test_binding_raises_what_a_flag_raises():
                  lambda: hs.cache_write(q, q, pages, pages, pos, pos, pos, interleaved=both)):
         with pytest.raises(RuntimeError, match="Boolean value"):
             call()
+
+
+def test_ragged_workspace_size_for_any_length(L):
+    """max_len 0 (any length) is enough for every length, as the calls take it."""
+    f = L.hysparse_ragged_workspace_size
+    for B, T, Hq, Hkv, most in ((1, 1, 8, 2, 1), (64, 64, 32, 8, 1), (3, 700, 64, 4, 300), (1, 40, 32, 1, 40),
+                                (16, 16, 64, 64, 1), (7, 30, 28, 4, 8), (1, 8192, 64, 4, 8192), (2, 64, 8, 2, 0)):
+        any_len = f(B, T, Hq, Hkv, 128, most, 0)
+        assert 256 <= any_len <= 94 << 20
+        for length in [1, 100, 999, 4096, 12345, 1 << 17, 1 << 20, 1 << 24] + [1 << i for i in range(31)]:
+            assert f(B, T, Hq, Hkv, 128, most, length) <= any_len, (B, T, Hq, Hkv, most, length)
