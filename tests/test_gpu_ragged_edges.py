@@ -182,3 +182,43 @@ def test_workspace_sized_without_lengths(T):
         for w in (ws, None):
             out, lse = hs.packed_attn(q.to(DEV), k.to(DEV), k.to(DEV), _int([0, T]), ws=w, **kw)
             ref.check_attend(str(kw), out, lse, ref.attend(q, k, k, SCALE))
+
+
+@pytest.mark.parametrize("by", [1, 10])
+def test_malformed_bounds_are_reported_each_time(by):
+    """Every kind of bad bound is reported by the call that met it, and sequences whose own bounds are
+    right are the definition's; few rows a sequence, and more."""
+    gen = torch.Generator().manual_seed(1)
+    hq, hkv, P, kv, T = 2, 1, 16, [40 * by, 33 * by, 20 * by], 7 * by
+    table, got = _paged(gen, kv, P, hkv, "bf16", stale=False)
+    q = torch.randn(T, hq, 128, generator=gen).to(BF)
+    a, b, c, d = 0, 2 * by, 5 * by, 7 * by
+    for longest in (max(kv), 64 * max(kv)):
+        n = hs.ragged_workspace_size(3, T, hq, hkv, 128, 3 * by, longest)
+        for rows, good in (([a, b, c, 900], (0, 1)), ([-4, b, c, d], (1, 2)), ([a, b, 2 ** 31 - 1, d], (0,)),
+                           ([-2 ** 31, b, c, d], (1, 2)), ([a, b, c, d + 1], (0, 1))):
+            ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+            out, lse = hs.chunk_attn_paged(q.to(DEV), got["k"][0], got["v"][0], _int(rows), _int(kv), table.to(DEV),
+                                           max_q=3 * by, max_len=longest, ws=ws)
+            assert hs.workspace_status(ws) == _lib.HS_ERR_INVALID_ARG, rows
+            for i in good:
+                part = slice(rows[i], rows[i + 1])
+                ref.check_attend(f"{rows} seq {i}", out[part], lse[:, part],
+                                 ref.attend(q[part], got["k"][2][i], got["v"][2][i], SCALE))
+
+
+def test_more_rows_than_announced_are_reported_by_each_kernel():
+    gen = torch.Generator().manual_seed(3)
+    hq, hkv, P, kv = 2, 1, 16, [40, 33, 20]
+    table, got = _paged(gen, kv, P, hkv, "bf16", stale=False)
+    q = torch.randn(600, hq, 128, generator=gen).to(BF)
+    # 9 tokens of 2 heads where a tile of 8 rows is planned; 3 + 2 items of 128 tokens where one a sequence is
+    for most, lens in ((1, [9, 0, 0]), (30, [300, 200, 0])):
+        cu = ref.cu_of(lens)
+        ws = torch.zeros(hs.ragged_workspace_size(3, sum(lens), hq, hkv, 128, most, 48), dtype=torch.uint8, device=DEV)
+        _chunk(q[:sum(lens)], got, cu, kv, table, max_q=most, max_len=48, ws=ws)
+        assert hs.workspace_status(ws) == _lib.HS_ERR_INVALID_ARG, most
+    ws = torch.zeros(hs.ragged_workspace_size(1, 600, hq, 1, 128, 200, 200), dtype=torch.uint8, device=DEV)
+    k = torch.randn(600, 1, 128, generator=gen).to(BF)
+    hs.packed_attn(q.to(DEV), k.to(DEV), k.to(DEV), _int([0, 600]), max_len=200, ws=ws)
+    assert hs.workspace_status(ws) == _lib.HS_ERR_INVALID_ARG
