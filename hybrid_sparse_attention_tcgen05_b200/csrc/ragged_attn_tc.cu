@@ -757,10 +757,14 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     pos.next(R::slots);
                     return slot;
                 };
-                // a slot is free after two commits: both issuers', or both of the only one that uses it
-                auto release = [&](int slot, bool alone) {
-                    commit_one(smem_u32(&bars->kv_empty[slot]), leader);
-                    if (alone) commit_one(smem_u32(&bars->kv_empty[slot]), leader);
+                // A slot is free once both issuers have let go of it: by a commit after the
+                // products that read it, or at once where it is the other's (solo).  That
+                // arrival keeps a slot from being filled again before this issuer has seen
+                // it full: two fills later the phase's parity would tell it nothing.
+                auto release = [&](int slot) { commit_one(smem_u32(&bars->kv_empty[slot]), leader); };
+                auto pass = [&](int slot) {
+                    if (leader) mbar_arrive(smem_u32(&bars->kv_empty[slot]));
+                    __syncwarp();
                 };
                 if (!wait(&bars->q_full, q_phase.take())) break;
                 // First both steps of the row tile's first key tile; then, step by step, P V
@@ -773,17 +777,20 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         qk(slot, 0);
                         qk(slot, 1);
                     }
-                    release(slot, false);
+                    release(slot);
                 } else {
                     // (the first two K tiles are row tile 0's and 1's; each issuer waits for
                     // the other's tiles too, or it would lose count of the slots' phases)
                     for (int j = 0; j < min(n, 2); ++j) {
                         if (!kv_wait()) break;
                         const int slot = take_slot();
-                        if (j != w) continue;
+                        if (j != w) {
+                            pass(slot);
+                            continue;
+                        }
                         qk(slot, 0);
                         qk(slot, 1);
-                        release(slot, true);
+                        release(slot);
                     }
                 }
                 // after the last product with Q; warpgroup 1 waits for issuer 0's before it
@@ -802,9 +809,10 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     if (!kv_wait()) break;
                     const int v = take_slot();
                     if (solo && !mine) {
+                        pass(v);
                         if (k_there) {
                             if (!kv_wait()) break;
-                            take_slot();
+                            pass(take_slot());
                         }
                         continue;
                     }
@@ -825,13 +833,13 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         if (!ok) break;
                         if (done + 1 == nw) release_q();
                     }
-                    release(v, solo);
+                    release(v);
                     if (k_there) {
                         if (k < 0) {                   // not needed here, but there to be released
                             if (!kv_wait()) break;
                             k = take_slot();
                         }
-                        release(k, solo);
+                        release(k);
                     }
                 }
             }
