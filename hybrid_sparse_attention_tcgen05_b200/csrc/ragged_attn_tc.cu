@@ -671,7 +671,9 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 k_tiles += n;
             }
             __syncwarp();
-            if (lane == 0 && *abort) {   // let our own copies land before the CTA goes away
+            // Let our own copies land before the CTA goes away.  Always: a wait of
+            // another warp may be given up after this one has found nothing to do.
+            if (lane == 0) {
                 if (q_loads > 0) mbar_drain(qb, (q_loads - 1) & 1);
                 for (uint32_t it = issued > (uint32_t)slots ? issued - slots : 0; it < issued; ++it)
                     mbar_drain(smem_u32(&full[it % slots]), (it / slots) & 1);

@@ -23,3 +23,22 @@ def test_rule_is_needed(rule, slots):
     with pytest.raises(Broken):
         for seed in range(200):
             _run(seed, slots, (rule,))
+
+
+def _late(block, running):
+    """A wait is given up after the producer has left."""
+    return "producer" not in running
+
+
+def _any_time(at):
+    turns = iter(range(10 ** 9))
+    return lambda block, running: next(turns) >= at
+
+
+def test_nothing_in_flight_after_giving_up():
+    for seed in range(200):
+        _run(seed, 4, give_up=_late)
+        _run(seed, 3, give_up=_any_time(random.Random(seed).randint(0, 1500)))
+    with pytest.raises(Broken, match="in flight"):
+        for seed in range(200):
+            _run(seed, 4, ("drain",), give_up=_late)
