@@ -188,11 +188,11 @@ attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                     tma_load_4d(smem_u32(skv + slot * TILE + hf * HALF), m, fb, hf * 64, g, (j_begin + j) * BN, b);
                 issued = it + 1;
             }
-            if (*abort) {  // let our own copies land before the CTA goes away
-                mbar_drain(qb, 0);
-                for (int it = issued > FWD_KV ? issued - FWD_KV : 0; it < issued; ++it)
-                    mbar_drain(smem_u32(&bars->kv_full[it % FWD_KV]), (it / FWD_KV) & 1);
-            }
+            // let our own copies land before the CTA goes away (always: another warp's
+            // wait may be given up after this)
+            mbar_drain(qb, 0);
+            for (int it = issued > FWD_KV ? issued - FWD_KV : 0; it < issued; ++it)
+                mbar_drain(smem_u32(&bars->kv_full[it % FWD_KV]), (it / FWD_KV) & 1);
         }
       } else if (warp == 9) {
         // ------------------------------------------------ MMA issuer
@@ -603,14 +603,13 @@ attn_scores_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     q_issued = it + 1;
                 }
             }
-            if (*abort) {
-                for (int j = k_issued > SC_K_STAGES ? k_issued - SC_K_STAGES : 0; j < k_issued; ++j)
-                    mbar_drain(smem_u32(&bars->k_full[j % SC_K_STAGES]), (j / SC_K_STAGES) & 1);
-                if (resident)
-                    for (int hh = 0; hh < G; ++hh) mbar_drain(smem_u32(&bars->q_full[hh]), 0);
-                for (int it = q_issued > SC_Q_STAGES ? q_issued - SC_Q_STAGES : 0; it < q_issued; ++it)
-                    mbar_drain(smem_u32(&bars->q_full[it % SC_Q_STAGES]), (it / SC_Q_STAGES) & 1);
-            }
+            // as in the full layer's producer: our copies land before the CTA goes away
+            for (int j = k_issued > SC_K_STAGES ? k_issued - SC_K_STAGES : 0; j < k_issued; ++j)
+                mbar_drain(smem_u32(&bars->k_full[j % SC_K_STAGES]), (j / SC_K_STAGES) & 1);
+            if (resident)
+                for (int hh = 0; hh < G; ++hh) mbar_drain(smem_u32(&bars->q_full[hh]), 0);
+            for (int it = q_issued > SC_Q_STAGES ? q_issued - SC_Q_STAGES : 0; it < q_issued; ++it)
+                mbar_drain(smem_u32(&bars->q_full[it % SC_Q_STAGES]), (it / SC_Q_STAGES) & 1);
         }
     } else if (warp == SC_MMA_WARP) {
         if (lane == 0) {

@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(THREADS) __maxnreg__(max_regs<NS>()) sparse_ga
                 ++seq;
             }
         }
-        if (lane == 0 && *abort) {
-            // let our own copies land before the CTA goes away
+        if (lane == 0) {
+            // let our own copies land before the CTA goes away (always: another warp's
+            // wait may be given up after this)
             for (int s2 = seq > NS ? seq - NS : 0; s2 < seq; ++s2)
                 mbar_drain(smem_u32(&bars->kv_full[s2 % NS]), (s2 / NS) & 1);
         }

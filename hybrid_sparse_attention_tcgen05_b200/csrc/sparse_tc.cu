@@ -138,11 +138,11 @@ sparse_dense_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     tma_load_4d(smem_u32(skv + slot * TILE + hf * HALF), m, fb, hf * 64, g, (it >> 1) * BN, b);
                 issued = it + 1;
             }
-            if (*abort) {
-                mbar_drain(qb, 0);
-                for (int it = issued > SD_KV ? issued - SD_KV : 0; it < issued; ++it)
-                    mbar_drain(smem_u32(&bars->kv_full[it % SD_KV]), (it / SD_KV) & 1);
-            }
+            // let our own copies land before the CTA goes away (always: another warp's
+            // wait may be given up after this)
+            mbar_drain(qb, 0);
+            for (int it = issued > SD_KV ? issued - SD_KV : 0; it < issued; ++it)
+                mbar_drain(smem_u32(&bars->kv_full[it % SD_KV]), (it / SD_KV) & 1);
         }
     } else if (warp == 5) {
         if (lane == 0) {
