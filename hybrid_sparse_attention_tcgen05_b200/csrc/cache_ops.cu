@@ -2,10 +2,13 @@
 // the write of new keys and values into paged caches (copied, or as 8-bit
 // floats under a power-of-two scale per row and head) and its counterpart
 // that reads rows back.  Each input byte is read once and each output byte
-// written once, in 16-byte accesses.  Rope and the read run at the copy's rate
-// (6.3 and 6.4 TB/s); the write does copied (16959 tokens of 8 heads 25.7 us,
-// 5.4 TB/s), but turning (37 us), 8-bit rows (34 us) or both (46 us) are bound
-// by instructions and by the chains of shuffles.
+// written once, in 16-byte accesses where the layout has them: 8-bit rows go in
+// 8 bytes a lane, rotated parts whose halves are no multiple of 16 bytes in
+// fewer, and the write reads a key again where half of its rotated part is no
+// multiple of 8 elements.  Rope and the read run at the copy's rate (6.3 and 6.4
+// TB/s); the write does copied (16959 tokens of 8 heads 25.7 us, 5.4 TB/s), but
+// turning (37 us), 8-bit rows (35 us) or both (47 us) are bound by instructions
+// and by the chains of shuffles.
 #include <atomic>
 
 #include <cuda_bf16.h>

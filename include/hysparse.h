@@ -271,9 +271,15 @@ int hysparse_block_paged(const hs_shape *shape, const int32_t *kv_len, const int
  * max_pages * page_size are below 2^31.
  * HS_E4M3 pools hold 8-bit floats (4 exponent bits, 3 mantissa bits) with one
  * scale byte per row and head in k_scale / v_scale [num_pages][Hkv][page_size]:
- * an element stands for code * 2^(byte - 127), bytes 1 to 254.  A power of
- * two makes every such value a bf16 number exactly.  Byte 255 marks a row of
- * NaN, whose codes are all NaN (0x7f or 0xff, which no other row holds). */
+ * an element stands for code * 2^(byte - 127), bytes 1 to 254.  With bytes 3 to
+ * 246 every such value is a bf16 number exactly.  Bytes 1 and 2 (rows whose
+ * largest magnitude is at most 448 * 2^-125): values are rounded to multiples of
+ * 2^-133 where rows are widened to bf16 (hysparse_cache_read to bf16, attention
+ * of many rows).
+ * Bytes from 247 on: codes that pass the largest float become infinity where rows
+ * are widened to bf16 or fp32; attention of few rows takes them as the numbers
+ * they stand for.  Byte 255 marks a row of NaN, whose codes are all NaN (0x7f or
+ * 0xff, which no other row holds). */
 typedef struct {
     const int32_t *cu_rows;       /* DEVICE [B + 1] */
     const int32_t *kv_len;        /* DEVICE [B]: positions in each cache, the new rows' among them */
@@ -310,8 +316,8 @@ int hysparse_rope(int T, int Hq, int Hkv, int d, int dtype, const void *q, long 
  * HS_E4M3 pools get, per row and head, the smallest power of two 2^e with
  * max|x| <= 448 * 2^e (2^0 for a row of zeros, e >= -126) as byte e + 127 and
  * the nearest 8-bit floats (ties to even) of x / 2^e; a row with a
- * NaN becomes a row of NaN, and an infinity 448 * 2^120, which widens to
- * infinity.  Other pool types get x rounded once.  Two rows of one call must not share a pool row.
+ * NaN becomes a row of NaN, and an infinity 448 * 2^120 (byte 247: see
+ * hs_paged_cache).  Other pool types get x rounded once.  Two rows of one call must not share a pool row.
  * ws (nullable) is only used for its status word.
  * Errors: HS_ERR_INVALID_ARG, HS_ERR_UNSUPPORTED, HS_ERR_CUDA. */
 int hysparse_cache_write(const hs_paged_cache *cache, int T, int Hkv, int d, int dtype, const void *k, long long ld_k,
