@@ -47,27 +47,35 @@ class Barrier:
 
 
 class Block:
-    """One CTA.  items: (key tiles, solo, tiles of row tile 0, of 1, whether each one's last half is unseen)."""
+    """One CTA.  items: (key tiles, solo, tiles of row tile 0, of 1, whether each one's last half is unseen).
+    f8: copies land in two staged tiles, and four warps widen them into a ring of three."""
 
-    def __init__(self, items, seed, slots=4, without=()):
+    def __init__(self, items, seed, f8=False, without=()):
+        slots = 3 if f8 else 4
         self.rng, self.items, self.slots, self.without = random.Random(seed), items, slots, without
         two = range(2)
         self.q_full, self.q_empty = Barrier("q_full", 1), Barrier("q_empty", 2 + 4)      # a warp arrives as one
-        self.kv_full = [Barrier(f"kv_full {i}", 1) for i in range(slots)]
+        self.kv_full = [Barrier(f"kv_full {i}", 4 if f8 else 1) for i in range(slots)]
         self.kv_empty = [Barrier(f"kv_empty {i}", 2) for i in range(slots)]
+        self.st_full = [Barrier(f"st_full {i}", 1 + 1) for i in two]                     # the tile; its scales
+        self.st_empty = [Barrier(f"st_empty {i}", 4) for i in two]
+        self.stage, self.f8 = [None, None], f8
         self.s_full = [[Barrier(f"s_full {w}{b}", 1) for b in two] for w in two]
         self.p_full = [[Barrier(f"p_full {w}{b}", 4) for b in two] for w in two]
         self.pv_done = [Barrier(f"pv_done {w}", 1) for w in two]
         self.o_full = [Barrier(f"o_full {w}", 1) for w in two]
         self.o_empty = [Barrier(f"o_empty {w}", 4) for w in two]
         self.work_full = [Barrier(f"work_full {i}", 1) for i in two]
-        self.work_empty = [Barrier(f"work_empty {i}", 11) for i in two]
+        self.work_empty = [Barrier(f"work_empty {i}", 15 if f8 else 11) for i in two]
         self.side_full, self.q_read = Barrier("side_full", 4), Barrier("q_read", 1)
         self.work, self.ring, self.q = [None, None], [None] * slots, None
         self.s, self.p = [[None, None], [None, None]], [[set(), set()], [set(), set()]]
         self.o, self.read_out = [None, None], [0, 0]
         self.pipe, self.copies, self.abort = [[], []], [], False
         self.agents = {"finder": self._role(self._finder()), "producer": self._role(self._producer(), self._copies_landed)}
+        if f8:
+            for i in range(4):
+                self.agents[f"widen {i}"] = self._role(self._widen(i))
         for w in two:
             self.agents[f"issuer {w}"] = self._role(self._issuer(w), lambda w=w: not self.pipe[w])
             for i in range(4):
@@ -134,12 +142,39 @@ class Block:
             order = [(j, v) for j in range(n) for v in (False, True)]
             if solo:              # K0 K1 V0 K2 V1 ... V(n-1)
                 order = [(0, False)] + [x for j in range(n) for x in ([(j + 1, False)] if j + 1 < n else []) + [(j, True)]]
+            full, empty, to = (self.st_full, self.st_empty, self.stage) if self.f8 else (self.kv_full, self.kv_empty, self.ring)
             for j, v in order:
-                slot = pos % self.slots
-                yield from self._wait_free(self.kv_empty[slot], pos // self.slots)
-                self.kv_full[slot].arrive(expect=1)
-                self.ring[slot] = None
-                self.copies.append((slot, (i, j, v), self.kv_full[slot]))
+                slot = pos % len(to)
+                yield from self._wait_free(empty[slot], pos // len(to))
+                full[slot].arrive(expect=1)
+                to[slot] = None
+                self.copies.append(((to, slot), (i, j, v), full[slot]))
+                if self.f8:
+                    yield None
+                    self.copies.append(((to, None), None, full[slot]))
+                    full[slot].bytes += 1             # the scales' arrival comes when they land
+                    full[slot].pending -= 1
+                pos += 1
+                yield None
+
+    def _widen(self, warp):
+        at, pos = [0], 0
+        while True:
+            item = yield from self._next(at)
+            if item is None:
+                return
+            for _ in range(2 * item[1]):
+                st, kv = pos % 2, pos % self.slots
+                yield from self._wait(self.st_full[st], pos // 2)
+                yield from self._wait_free(self.kv_empty[kv], pos // self.slots)
+                tile = self.stage[st]
+                yield None
+                if self.stage[st] != tile or tile is None:
+                    raise Broken(f"a staged tile is {self.stage[st]}, was {tile}")
+                parts = self.ring[kv] if isinstance(self.ring[kv], dict) and len(self.ring[kv]) < 4 else {}
+                self.ring[kv] = {**parts, warp: tile}
+                self.kv_full[kv].arrive()
+                self.st_empty[st].arrive()
                 pos += 1
                 yield None
 
@@ -300,15 +335,18 @@ class Block:
             yield None
 
     # ---- what ends at a time of its own
+    def _holds(self, slot, tile):
+        return self.ring[slot] == (dict.fromkeys(range(4), tile) if self.f8 else tile)
+
     def _product_qk(self, w, i, slot, h, j):
-        if self.ring[slot] != (i, j, False) or self.q != i:
+        if not self._holds(slot, (i, j, False)) or self.q != i:
             raise Broken(f"Q K^T of item {i} tile {j} reads {self.ring[slot]} and Q of {self.q}")
         if self.p[w][h]:
             raise Broken(f"Q K^T of item {i} tile {j} overwrites P")
         self.s[w][h] = (i, j, h)
 
     def _product_pv(self, w, i, slot, h, j, first):
-        if self.ring[slot] != (i, j, True) or self.p[w][h] != {(i, j, h, x) for x in range(4)}:
+        if not self._holds(slot, (i, j, True)) or self.p[w][h] != {(i, j, h, x) for x in range(4)}:
             raise Broken(f"P V of item {i} tile {j} reads {self.ring[slot]} and P of {self.p[w][h]}")
         self.p[w][h] = set()
         if first:
@@ -318,11 +356,11 @@ class Block:
         self.o[w][1].append((j, h))
 
     def _copy_lands(self):
-        slot, what, bar = self.copies.pop(self.rng.randrange(len(self.copies)))
-        if slot is None:
+        place, what, bar = self.copies.pop(self.rng.randrange(len(self.copies)))
+        if place is None:
             self.q = what
-        else:
-            self.ring[slot] = what
+        elif place[1] is not None:
+            place[0][place[1]] = what
         bar.landed()
 
     def run(self, give_up=None):
