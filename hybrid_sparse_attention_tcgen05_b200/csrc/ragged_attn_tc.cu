@@ -28,7 +28,7 @@
 //   12-15     8-bit caches only: widen staged rows to bf16 tiles.  A code
 //             times a power of two from 2^-124 to 2^119 is a bf16 number, so
 //             nothing is rounded there.  Their instructions are what bounds
-//             8-bit chunks (435 to 450 us for 4 of 1000 over 12000, 365 to 377
+//             8-bit chunks (430 to 435 us for 4 of 1000 over 12000, 365 to 377
 //             with bf16 pages).
 // TMEM (512 columns): two S buffers of 64 keys for each row tile, then O0 and
 // O1.  A key tile is taken in two steps of 64 keys, so that S of the next step
@@ -104,8 +104,8 @@ struct RaggedBars {
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
-    uint32_t bad_any[kBadBufs];           // K tile i of the CTA has keys on pages outside the pool: bad[i % 8] says which
-    uint32_t bad[kBadBufs][4];
+    uint32_t bad_any[kBadBufs];           // K tile i of the CTA has boxes on pages outside the pool: bad[i % 8] says which
+    uint32_t bad[kBadBufs][4];            // (a bit for each box)
     uint8_t scale[2][128];                // scale bytes of the staged tiles
     float2 side[128];                     // solo: warpgroup 1's maximum and sum of each row
     Work work[2];
@@ -628,28 +628,28 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const int boxes = p.paged ? (min(BN, wk.kvl - key0) + p.box_rows - 1) >> rshift : 1;
                     int page = 0;
                     if (p.paged && lane < boxes) page = __ldg(table + ((key0 + (lane << rshift)) >> p.c.page_shift));
+                    if (!is_v && p.paged) {
+                        const int bad = (k_tiles + j) % kBadBufs;
+                        // Which boxes lie on pages outside the pool, for the softmax to leave
+                        // their keys out.  By the lane that arrives on the barrier below, before
+                        // it does: the copies' bytes order nothing before the readers.
+                        uint32_t any = 0;
+#pragma unroll 1
+                        for (int w = 0; w < boxes; w += 32) {
+                            const int i = w + lane;
+                            int pg = page;
+                            if (w > 0 && i < boxes) pg = __ldg(table + ((key0 + (i << rshift)) >> p.c.page_shift));
+                            const uint32_t out = __ballot_sync(0xffffffffu, i < boxes && (pg < 0 || pg >= p.c.num_pages));
+                            if (lane == 0) bars->bad[bad][w >> 5] = out;
+                            any |= out;
+                        }
+                        if (lane == 0) bars->bad_any[bad] = any;
+                    }
                     ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&empty[pos.slot]), pos.phase ^ 1, p.wait_ns, abort));
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[pos.slot]);
                     const uint32_t dst = smem_u32(F8 ? sst + pos.slot * kStage : skv + pos.slot * TILE);
                     const CUtensorMap *m = is_v ? &tv : &tk;
-                    const int bad = (k_tiles + j) % kBadBufs;
-                    if (!is_v && p.paged) {
-                        // Which keys lie on pages outside the pool, for the softmax to leave
-                        // out.  Written before the barrier's arrival below, which is what
-                        // the readers are ordered behind: the copies' bytes order nothing.
-                        if (lane == 0) bars->bad_any[bad] = 0;
-                        if (lane < 4) bars->bad[bad][lane] = 0;
-                        __syncwarp();
-                        for (int i = lane; i < boxes; i += 32) {
-                            const int pg = i < 32 ? page : __ldg(table + ((key0 + (i << rshift)) >> p.c.page_shift));
-                            if (pg >= 0 && pg < p.c.num_pages) continue;
-                            bars->bad_any[bad] = 1;
-                            for (int r = i << rshift; r < (i + 1) << rshift; ++r)
-                                atomicOr(&bars->bad[bad][r >> 5], 1u << (r & 31));
-                        }
-                        __syncwarp();
-                    }
                     if (lane == 0) mbar_expect_tx(fb, (uint32_t)(boxes * p.box_rows * parts * row_bytes));
                     __syncwarp();
                     for (int i = lane; i < boxes; i += 32) {
@@ -984,7 +984,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     if (lost) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const uint32_t bits = bars->bad[bad][2 * buf + q];
+                            const int c = 64 * buf + 32 * q + lane, box = c >> (31 - __clz(p.box_rows));
+                            const uint32_t bits = __ballot_sync(0xffffffffu, (bars->bad[bad][box >> 5] >> (box & 31)) & 1u);
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if ((bits >> c) & 1u) s[32 * q + c] = -INFINITY;
