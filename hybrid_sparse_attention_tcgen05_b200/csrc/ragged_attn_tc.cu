@@ -1196,7 +1196,8 @@ ragged_attn_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         }
         // a wait gave up: the rows of the items that this CTA did not get to
         // are marked like those of the one it was at
-        if (*abort && (warp & 3) == 0) {
+        // (one answer for the warp: its lanes look for the items together)
+        if (__any_sync(0xffffffffu, *abort != 0) && (warp & 3) == 0) {
             const Batch bt = read_batch(p);
             for (int i = work_i;; ++i) {
                 const Work x = find_work(p, bt, i);
